@@ -223,7 +223,8 @@ def _prepare_cache(c, gen, device):
     if own:
         from sparse_rank_attention_block_b200 import sda
         s["p"] = sda.cache_params(B=B, H=H, H_kv=H_kv, d=d, block=block, n_blocks=n_blocks,
-                                  max_blocks=s["table"].shape[1], rows=T, max_new=max(new), keep=keep, recent=recent)
+                                  max_blocks=s["table"].shape[1], rows=T, max_new=max(new),
+                                  weights=c.get("weights", False), keep=keep, recent=recent)
         s["ws"] = sda.Workspace(s["p"], device=device)
     return s
 
