@@ -298,6 +298,136 @@ int32_t sda_forward_host(const sda_params* p, const uint16_t* q_host, const uint
                          const uint16_t* p_k_host, const float* g_host, uint16_t* o_host,
                          void* dev_buf, size_t dev_buf_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving operators: attention over whole prompts, and a key/value cache held
+ * in 8 bits with its append, its attention and its eviction. They have no
+ * counterpart in the pages (whose causal window, robotworld summary section 4,
+ * is for generation chunk by chunk); the formulas are stated here in full.
+ *
+ * Shared by all five calls, besides the conventions at the top of this file:
+ *  - H query heads share H_kv key heads in order: query head h reads key head
+ *    h / (H / H_kv); H_kv must divide H. d in {64, 128}; bf16 rows.
+ *  - Sequences are packed: the rows of sequence s are seq[s] .. seq[s+1] - 1
+ *    of the tensors, seq being n + 1 ascending int32 on the device. Rows
+ *    before the first and behind the last sequence are neither used nor
+ *    written. A sequence may have no rows.
+ *  - A row of q, k, v or o is [heads, d] elements; ld_* is the distance
+ *    between rows in elements (0: dense), a multiple of 8 and at least
+ *    heads * d, so that slices of one projection's output can be passed.
+ *  - scale is the softmax scale (> 0, finite; 0: 1 / sqrt(d)).
+ *  - Device-side arguments (offsets, lengths, block numbers) are checked on
+ *    the device: what does not fit is clamped or left out, never read or
+ *    written out of range, and reported as SDA_ERR_SHAPE by sda_read_status.
+ *    Which outputs are then undefined each call says. Other pointers have to be
+ *    in the memory of the device that is current.
+ *  - Sums, maxima and running states are fp32; every sum has a fixed order
+ *    (bit-identical reruns).
+ *  - `ws`: sda_prompt_workspace_size() / sda_cache_workspace_size() bytes,
+ *    256-byte aligned, passed through sda_workspace_init once. Calls that may
+ *    run at the same time (other streams, graphs) need workspaces of their own.
+ * ------------------------------------------------------------------------- */
+
+typedef struct sda_prompt_params {
+  int32_t n_seq;             /* packed sequences, 1..65535 */
+  int32_t rows_q, rows_k;    /* rows of q and o, rows of k and v */
+  int32_t H, H_kv, d;
+  int32_t causal;            /* 1: key j is visible to query i iff j <= i + n_k - n_q; 0: all keys are */
+  int64_t ld_q, ld_k, ld_v, ld_o;
+  double scale;
+} sda_prompt_params;
+
+size_t sda_prompt_workspace_size(const sda_prompt_params* p);
+
+/* Attention over whole prompts. For query row i (0..n_q-1) and head h of a
+ * sequence with n_q rows of q and n_k rows of k and v:
+ *   p_ij = exp(scale q_i . k_j) / sum_j' exp(scale q_i . k_j'),
+ *   o_i = sum_j p_ij v_j,  lse_i = ln sum_j' exp(scale q_i . k_j')
+ * over its visible keys. With n_k > n_q the queries are the last n_q positions
+ * (a prompt's later chunk). A row that sees no key gets o = 0, lse = -inf.
+ * P is rounded to bf16 before the product with V (fp32 accumulation).
+ * q: [rows_q, H, d], k, v: [rows_k, H_kv, d], o: [rows_q, H, d] bf16; lse:
+ * [rows_q, H] fp32 or NULL. k and v rows of a sequence must be finite (a
+ * hidden key's infinity may reach rows that do not see it); rows outside the
+ * sequences may hold anything. Bad offsets: the sequences' outputs are
+ * undefined. */
+int32_t sda_prompt_attn_fwd(const sda_prompt_params* p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                            const int32_t* seq_q, const int32_t* seq_k, uint16_t* o, float* lse, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/* The cache: a pool of n_blocks blocks of `block` tokens. k_codes, v_codes:
+ * [n_blocks, H_kv, block, d] E4M3 bytes; k_scale, v_scale: [n_blocks, H_kv]
+ * fp32, a value being its code times the scale of its block and head; w (where
+ * weights are collected): [n_blocks, H_kv, block] fp32. block_table: [B,
+ * max_blocks] int32, the pool's block that holds tokens t * block .. of a
+ * sequence; entries behind the sequence's last block are not read. lens: [B]
+ * int32, tokens of each sequence (including the new ones in append and
+ * attention). */
+typedef struct sda_cache_params {
+  int32_t B;                 /* sequences, 1..65535 */
+  int32_t H, H_kv, d;
+  int32_t block;             /* tokens per block: 16, 32, 64 or 128 */
+  int32_t n_blocks;          /* blocks in the pool */
+  int32_t max_blocks;        /* width of block_table */
+  int32_t rows;              /* rows of q and o (attention), of k and v (append); eviction: not used */
+  int32_t max_new;           /* most new tokens of one sequence, >= 1 (append, attention) */
+  int32_t weights;           /* 1: attention may collect weights (its workspace then holds all scores) */
+  int32_t keep, recent;      /* eviction: tokens that stay, the newest among them that always do (0 <= recent <= keep) */
+  int64_t ld_q, ld_k, ld_v, ld_o;
+  double scale;
+} sda_cache_params;
+
+size_t sda_cache_workspace_size(const sda_cache_params* p);
+
+/* Append. The n_b = seq[b+1] - seq[b] rows of k and v (n_b <= max_new) become
+ * tokens lens[b] - n_b .. lens[b] - 1 of sequence b. For each touched block and
+ * head, and for K and V apart: with amax the largest finite magnitude among the
+ * new tokens, the wanted scale is the smallest power of two s >= 2^-126 with
+ * amax <= 448 s (at most 2^120); the block's scale becomes the larger of it and, where
+ * older tokens are in the block, of its scale so far, and those tokens' codes
+ * are written anew under it (exact but for values that become subnormal). New
+ * codes are E4M3(x / scale), nearest even; infinities saturate, NaN stays NaN.
+ * A power of two costs an 8-bit float no precision. Slots behind the last
+ * token stay as they are. w (or NULL): set to zero at the new tokens. Blocks
+ * must not be shared between sequences that write to them. Rows that do not
+ * fit (n_b > max_new, lens[b] < n_b, lens[b] > max_blocks * block, a block
+ * number outside the pool) are left out and reported. */
+int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uint16_t* v, const int32_t* seq,
+                         const int32_t* lens, const int32_t* block_table, uint8_t* k_codes, uint8_t* v_codes,
+                         float* k_scale, float* v_scale, float* w, void* ws, size_t ws_bytes, void* stream);
+
+/* Attention over the cache. Row i of the n_b rows of q of sequence b (n_b <=
+ * max_new) is its token lens[b] - n_b + i and sees tokens 0 .. that one (append
+ * its key first): o as in sda_prompt_attn_fwd, with the cache's values; a row
+ * at a negative position sees nothing and gets zeros. Products of q (bf16,
+ * brought to fp16 by an exact power of two per row) with the codes are exact,
+ * P is rounded to fp16.
+ * w_out (or NULL; needs weights = 1): w_out[slot] = w_in[slot] + the sum of the token's p over the
+ * call's rows and the key head's query heads, for every token of the B
+ * sequences; other slots of w_out stay as they are. w_in NULL counts as zeros;
+ * w_in may be w_out. Rows over max_new, tokens in blocks outside the pool and
+ * tokens past max_blocks * block are left out and reported. NaN or infinity in a
+ * cached token reaches the rows of its sequence. */
+int32_t sda_cache_attn_fwd(const sda_cache_params* p, const uint16_t* q, const int32_t* seq, const int32_t* lens,
+                           const int32_t* block_table, const uint8_t* k_codes, const uint8_t* v_codes,
+                           const float* k_scale, const float* v_scale, const float* w_in, float* w_out,
+                           uint16_t* o, void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction by collected weight. For every sequence b and key head: of its
+ * lens[b] tokens n = min(lens[b], keep) stay: the newest min(recent, n) and,
+ * of the older ones, those with the largest w (ties to the lower position; NaN
+ * counts as the largest). They keep their order and become tokens 0 .. n - 1 of
+ * the blocks dst_table[b, :] ([B, ceil(keep / block)], other blocks than those
+ * of block_table; n tokens' blocks are read, the rest may be -1). A target
+ * block's scale is the largest of its tokens' source scales, codes are written
+ * anew under it as in append, w moves along; slots behind the last token stay
+ * as they are. kept: [B, H_kv, keep] int32, the positions that stayed,
+ * ascending, -1 behind them; dst_lens: [B] int32, n. Sources are not changed.
+ * Tokens whose block is outside the pool are left out and reported (their
+ * targets are undefined). */
+int32_t sda_cache_evict(const sda_cache_params* p, const int32_t* lens, const int32_t* block_table, uint8_t* k_codes,
+                        uint8_t* v_codes, float* k_scale, float* v_scale, float* w, const int32_t* dst_table,
+                        int32_t* kept, int32_t* dst_lens, void* ws, size_t ws_bytes, void* stream);
+
 /* Failure-detection diagnostic: sets the time limit, in nanoseconds, of the
  * waits on pipeline progress (TMA tiles landed, MMAs done, softmax tiles
  * handed over) in the tcgen05 sparse attention kernel of sda_sparse_attn_fwd

@@ -1,0 +1,567 @@
+// Attention over whole prompts on the 5th-generation tensor cores (tcgen05):
+// packed sequences of different lengths, shared key heads, causal or all to
+// all. For query row i of a sequence with n_q queries and n_k keys
+//   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j) / sum_j' exp(scale q_i . k_j')
+// over the keys j <= i + n_k - n_q (causal) or all n_k keys; a row that sees
+// no key gives zeros and lse = -inf.
+//
+// Bound by the tensor pipe and, as closely, by the exponential unit: a
+// 128 x 128 tile at d = 128 takes 1024 cycles of MMA (S = Q K^T and O += P V)
+// and 1024 cycles of MUFU. One CTA per SM therefore carries TWO 128-row tiles
+// that share every K and V tile: the tensor pipe works on one while the
+// softmax warps work on the other. The two tiles are two query heads of the
+// same key head (equal work under the causal mask) or, where the heads of a
+// key head are odd in number, two adjacent row tiles of one head.
+//
+// Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 issues every
+// MMA, 2 finds the CTA's tile and owns TMEM, 3 clears V rows behind the
+// sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1, a thread per row.
+//
+// The MMAs of one thread execute in order, so the issue order
+//   PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)
+// lets P_w overlay S_w in TMEM (bf16, half the columns): QK_w(j+1) comes
+// after PV_w(j) has read P_w, and S_w(j+1) ready implies PV_w(j) done, so the
+// softmax may rescale O_w without another wait. It does so only when a row's
+// maximum grows by more than 2^8 (exact: numerator and denominator share the
+// reference). P is rounded to bf16 (the type of V, as the MMA asks); the sum
+// takes the unrounded fp32 values.
+//
+// TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+d), O_1 [384,384+d).
+// Shared memory: Q_0, Q_1 (later the output tiles), kStages tiles of K or V.
+//
+// Rows of K and V behind the sequence belong to other sequences or to nobody:
+// their scores are replaced before use and their V rows are cleared in shared
+// memory, so nothing there (infinities, NaN) reaches an output. Rows of O
+// behind the sequence are not written.
+//
+// Every wait is bounded; a CTA that gives up reports through the status word,
+// drains its loads and MMAs, frees TMEM and exits.
+
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "ex2_fma.cuh"
+#include "serving.h"
+#include "tc.cuh"
+
+namespace sda {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;  // query rows of a tile, keys of a step
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * tile
+constexpr int kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
+static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kRegsLaunch * kThreads, "register split exceeds the launch");
+
+template <int D>
+struct Smem {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTileBytes = kHalves * kTile * 128;  // [half][128 rows][128 B]
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + 2 * kTileBytes;
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kTotal = kBars + 512;
+};
+
+enum { B_QFULL = 0, B_SFULL = 2, B_PFULL = 4, B_ODONE = 6, B_VLAST = 8, B_VCLEAR = 9, B_DRAIN = 10, B_FULL = 11 };  // + ring full, ring empty
+
+// What the CTA works on, found by one warp.
+struct Item {
+  int valid;
+  int q0, nq, k0, nk;  // the sequence's rows of q and of k
+  int t;               // row tile within the sequence
+};
+
+struct Span {
+  int q0, nq, k0, nk;
+};
+
+// Sequence s with offsets clamped into the tensors; `bad` when they were not.
+__device__ __forceinline__ Span span_of(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int s, bool& bad) {
+  const int qa = __ldg(seq_q + s), qb = __ldg(seq_q + s + 1), ka = __ldg(seq_k + s), kb = __ldg(seq_k + s + 1);
+  Span r;
+  r.q0 = min(max(qa, 0), p.rows_q);
+  r.nq = min(max(qb, r.q0), p.rows_q) - r.q0;
+  r.k0 = min(max(ka, 0), p.rows_k);
+  r.nk = min(max(kb, r.k0), p.rows_k) - r.k0;
+  bad = bad || r.q0 != qa || r.q0 + r.nq != qb || r.k0 != ka || r.k0 + r.nk != kb;
+  return r;
+}
+
+// Keys that the rows below `end` of a sequence may see.
+__device__ __forceinline__ int keys_below(const Prompt& p, const Span& s, int end) {
+  return p.causal ? max(0, min(s.nk, end + s.nk - s.nq)) : s.nk;
+}
+
+// Row tiles (of R rows) of a sequence whose key steps number more than x.
+__device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int R, int x) {
+  const int T = (s.nq + R - 1) / R;
+  if (x < 0) return T;
+  if (!p.causal) return s.nk > kTile * x ? T : 0;
+  if (s.nk <= kTile * x) return 0;  // the last tile sees all nk keys, none sees more
+  // tile t (not the last) sees (t + 1) R + nk - nq keys
+  const int need = kTile * x - (s.nk - s.nq);
+  const int first = need < 0 ? 0 : need / R;
+  return T - min(first, T - 1);
+}
+
+// The CTA's row tile. Tiles go out heaviest first (most key steps), so that
+// the last ones to start are short: tile i of the order has the step count x
+// with over(x) <= i < over(x - 1), over(x) the number of tiles of more than x
+// steps, found by bisection; among equals, sequences in order.
+__device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int R, int i, Item* out,
+                          bool& bad) {
+  const int lane = threadIdx.x & 31;
+  Span mine{0, 0, 0, 0};
+  if (lane < p.n_seq) mine = span_of(p, seq_q, seq_k, lane, bad);
+  auto over = [&](int x) {
+    int n = lane < p.n_seq ? tiles_over(p, mine, R, x) : 0;
+    for (int s = 32 + lane; s < p.n_seq; s += 32) n += tiles_over(p, span_of(p, seq_q, seq_k, s, bad), R, x);
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  int top = lane < p.n_seq ? mine.nk : 0;
+  for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
+  top = __reduce_max_sync(0xffffffffu, top);
+  out->valid = 0;
+  if (i >= over(-1)) return;
+  int lo = 0, hi = (top + kTile - 1) / kTile;  // over(hi) = 0 <= i
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (over(mid) <= i) hi = mid;
+    else lo = mid + 1;
+  }
+  int rest = i - over(lo);  // number among the tiles of exactly lo steps
+  for (int base = 0; base < p.n_seq; base += 32) {
+    const int s = base + lane;
+    Span sp = base == 0 ? mine : Span{0, 0, 0, 0};
+    if (base > 0 && s < p.n_seq) sp = span_of(p, seq_q, seq_k, s, bad);
+    const int above = s < p.n_seq ? tiles_over(p, sp, R, lo) : 0;
+    const int n = s < p.n_seq ? tiles_over(p, sp, R, lo - 1) - above : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (rest >= sum - n && rest < sum) {
+      out->q0 = sp.q0;
+      out->nq = sp.nq;
+      out->k0 = sp.k0;
+      out->nk = sp.nk;
+      out->t = (sp.nq + R - 1) / R - 1 - above - (rest - (sum - n));
+      out->valid = 1;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    if (rest < all) break;
+    rest -= all;
+  }
+}
+
+__device__ __forceinline__ uint32_t sw(uint32_t row, uint32_t chunk) { return tc::sw128_offset(row, chunk); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, Prompt p, int pair_heads,
+                   const int32_t* __restrict__ seq_q, const int32_t* __restrict__ seq_k, uint16_t* __restrict__ o,
+                   float* __restrict__ lse, unsigned* status, uint64_t wait_ns) {
+  using S = Smem<D>;
+  constexpr int NS = S::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  uint64_t* full = bars + B_FULL;
+  uint64_t* empty = full + NS;
+  unsigned char* tail = smem + S::kBars + 8 * (B_FULL + 2 * NS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
+  int* bad_flag = reinterpret_cast<int*>(tail + 8);
+  Item* item = reinterpret_cast<Item*>(tail + 16);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int groups = pair_heads ? p.H / 2 : p.H;  // head groups, fastest: they share the tile's K and V through L2
+  const int hg = blockIdx.x % groups;
+  const int R = pair_heads ? kTile : 2 * kTile;
+
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&bars[B_QFULL + w], 1);
+      tc::mbar_init(&bars[B_SFULL + w], 1);
+      tc::mbar_init(&bars[B_PFULL + w], 128);
+      tc::mbar_init(&bars[B_ODONE + w], 1);
+    }
+    tc::mbar_init(&bars[B_VLAST], 1);
+    tc::mbar_init(&bars[B_VCLEAR], 32);
+    tc::mbar_init(&bars[B_DRAIN], 1);
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    *abort_flag = (*reinterpret_cast<volatile unsigned*>(status) & kStatusTimeout) ? 1 : 0;
+    *bad_flag = 0;
+    tc::fence_mbar_init();
+    tc::tma_prefetch(&tm_q);
+    tc::tma_prefetch(&tm_k);
+    tc::tma_prefetch(&tm_v);
+  }
+  if (warp == 2) {
+    bool bad = false;
+    find_item(p, seq_q, seq_k, R, blockIdx.x / groups, item, bad);
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report_status(status, kStatusBadIndex);
+  }
+  __syncthreads();
+  if (*abort_flag || !item->valid) return;  // uniform
+  if (warp == 2) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  const Span seq{item->q0, item->nq, item->k0, item->nk};
+  const int row0 = item->t * R;
+  const int h0 = pair_heads ? 2 * hg : hg;
+  const int h_kv = h0 / (p.H / p.H_kv);
+  // tile w: rows [row_w, end_w) of the sequence, head h_w, steps n_w (0: nothing visible)
+  const int row_1 = pair_heads ? row0 : row0 + kTile;
+  const int end_0 = min(row0 + kTile, seq.nq), end_1 = min(row_1 + kTile, seq.nq);
+  const bool live_1 = row_1 < seq.nq;
+  const int n0 = (keys_below(p, seq, end_0) + kTile - 1) / kTile;
+  const int n1 = live_1 ? (keys_below(p, seq, end_1) + kTile - 1) / kTile : 0;
+  const int n = max(n0, n1);
+
+  if (warp < 4) {
+    tc::setmaxnreg_dec<kRegsLow>();
+    volatile int never = 0;
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ loads
+      bool ok = true;
+      for (int w = 0; w < 2; ++w) {
+        if ((w ? n1 : n0) == 0) continue;
+        tc::mbar_arrive_expect_tx(&bars[B_QFULL + w], S::kTileBytes);
+        for (int hf = 0; hf < S::kHalves; ++hf)
+          tc::tma_load_3d(smem + S::kQ + w * S::kTileBytes + hf * kTile * 128, &tm_q, &bars[B_QFULL + w], 64 * hf,
+                          pair_heads ? h0 + w : h0, seq.q0 + (w ? row_1 : row0));
+      }
+      // ring order K_0, V_0, K_1, V_1, ...: the order in which the MMAs release them
+      int c = 0;
+      for (; c < 2 * n; ++c) {
+        const int st = c % NS;
+        if (c >= NS) ok = tc::wait1(&empty[st], (c / NS - 1) & 1, abort_flag, wait_ns);
+        if (!ok) break;
+        // the last V tile has a barrier of its own: another warp waits for it, from the start
+        uint64_t* bar = c == 2 * n - 1 ? &bars[B_VLAST] : &full[st];
+        tc::mbar_arrive_expect_tx(bar, S::kTileBytes);
+        for (int hf = 0; hf < S::kHalves; ++hf)
+          tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + hf * kTile * 128, c % 2 == 0 ? &tm_k : &tm_v, bar,
+                          64 * hf, h_kv, seq.k0 + c / 2 * kTile);
+      }
+      // no load is in flight when the CTA ends, whatever the others did
+      for (int w = 0; w < 2; ++w)
+        if ((w ? n1 : n0) > 0) tc::wait1(&bars[B_QFULL + w], 0, &never);
+      for (int b = c > NS ? c - NS : 0; b < c; ++b)
+        tc::wait1(b == 2 * n - 1 ? &bars[B_VLAST] : &full[b % NS], b == 2 * n - 1 ? 0 : (b / NS) & 1, &never);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      constexpr uint32_t idesc_qk = tc::idesc_bf16(128, 128, false);
+      constexpr uint32_t idesc_pv = tc::idesc_bf16(128, D, true);  // B = V, MN-major
+      bool ok = true;
+      auto stage_of = [&](int c) { return smem + S::kRing + (c % NS) * S::kTileBytes; };
+      auto wait_full = [&](int c) { return tc::wait1(&full[c % NS], (c / NS) & 1, abort_flag, wait_ns); };
+      auto qk = [&](int w, int j) {
+        const unsigned char* kst = stage_of(2 * j);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int hf = kk / 4, c = kk % 4;
+          const uint64_t da =
+              tc::smem_desc_sw128(smem + S::kQ + w * S::kTileBytes + hf * kTile * 128 + c * 32, 16, 1024);
+          const uint64_t db = tc::smem_desc_sw128(kst + hf * kTile * 128 + c * 32, 16, 1024);
+          tc::mma_ss(tmem + kColS + 128 * w, da, db, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(&bars[B_SFULL + w]);
+      };
+      if (n > 0) ok = wait_full(0);
+      for (int w = 0; w < 2 && ok; ++w) {
+        if ((w ? n1 : n0) == 0) continue;
+        ok = tc::wait1(&bars[B_QFULL + w], 0, abort_flag, wait_ns);
+        if (!ok) break;
+        tc::fence_after_sync();
+        qk(w, 0);
+      }
+      if (ok && n > 0) tc::commit(&empty[0]);
+      for (int j = 0; j < n && ok; ++j) {
+        const int cv = 2 * j + 1, ck = 2 * j + 2;
+        const unsigned char* vst = stage_of(cv);
+        ok = j == n - 1 ? tc::wait1(&bars[B_VCLEAR], 0, abort_flag, wait_ns) : wait_full(cv);
+        bool have_k = false;
+        for (int w = 0; w < 2 && ok; ++w) {
+          const int nw = w ? n1 : n0;
+          if (j >= nw) continue;
+          ok = tc::wait1(&bars[B_PFULL + w], j & 1, abort_flag, wait_ns);
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            const uint64_t db = tc::smem_desc_sw128(vst + kk * 16 * 128, kTile * 128, 1024);
+            tc::mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db, idesc_pv,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          if (j == nw - 1) tc::commit(&bars[B_ODONE + w]);
+          if (j + 1 < nw) {
+            if (!have_k) ok = wait_full(ck);
+            if (!ok) break;
+            have_k = true;
+            qk(w, j + 1);
+          }
+        }
+        if (!ok) break;
+        tc::commit(&empty[cv % NS]);
+        if (j + 1 < n) tc::commit(&empty[ck % NS]);
+      }
+      // drain: every MMA this thread issued
+      tc::commit(&bars[B_DRAIN]);
+      tc::wait1(&bars[B_DRAIN], 0, &never);
+    } else if (warp == 3 && n > 0) {
+      // ------------------------------------------------------------ V rows behind the sequence
+      const int c = 2 * n - 1;  // the last V tile
+      const bool ok = tc::wait_warp(&bars[B_VLAST], 0, abort_flag, wait_ns);
+      const int valid = seq.nk - (n - 1) * kTile;
+      if (ok && valid < kTile) {
+        unsigned char* vst = smem + S::kRing + (c % NS) * S::kTileBytes;
+        for (int e = valid * 8 * S::kHalves + lane; e < kTile * 8 * S::kHalves; e += 32) {
+          const int row = e / (8 * S::kHalves), ch = e % (8 * S::kHalves);
+          *reinterpret_cast<uint4*>(vst + (ch / 8) * kTile * 128 + row * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        tc::fence_proxy_async_smem();
+      }
+      tc::mbar_arrive(&bars[B_VCLEAR]);
+    }
+  } else {
+    tc::setmaxnreg_inc<kRegsHigh>();
+    // ------------------------------------------------------------ softmax of tile w, epilogue
+    const int w = warp < 8 ? 0 : 1;
+    const int quarter = warp & 3;
+    const int row = 32 * quarter + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t t_s = tmem + lane_base + kColS + 128 * w;
+    const uint32_t t_o = tmem + lane_base + kColO + 128 * w;
+    const int nw = w ? n1 : n0;
+    const int tile_row = w ? row_1 : row0;
+    const int my_row = tile_row + row;               // row of the sequence
+    const int lim = keys_below(p, seq, my_row + 1);  // keys this row sees (rows behind the sequence: all)
+    const int lim_first = keys_below(p, seq, tile_row + 1);
+    bool ok = true;
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < nw; ++j) {
+      ok = tc::wait_warp(&bars[B_SFULL + w], j & 1, abort_flag, wait_ns);
+      if (!ok) break;
+      tc::fence_after_sync();
+      float s[128];
+      {
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32p(t_s + 32 * c, sr + 32 * c);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(sr[c]);
+      }
+      if ((j + 1) * kTile > lim_first) {  // some row of the tile does not see all of the step's keys
+        const int vis = lim - j * kTile;
+#pragma unroll
+        for (int c = 0; c < 128; ++c) s[c] = c < vis ? s[c] : -INFINITY;
+      }
+      float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
+#pragma unroll
+      for (int c = 8; c < 128; c += 8) {
+        a0 = max3(a0, s[c], s[c + 1]);
+        a1 = max3(a1, s[c + 2], s[c + 3]);
+        a2 = max3(a2, s[c + 4], s[c + 5]);
+        a3 = max3(a3, s[c + 6], s[c + 7]);
+      }
+      const float mx = max3(a0, a1, fmaxf(a2, a3)) * p.scale_log2;
+      if (j == 0) {
+        m = mx;
+      } else {
+        const bool grow = mx > m + 8.0f;
+        if (__any_sync(0xffffffffu, grow)) {
+          // S_w(j) ready: PV_w(j - 1) is done and O_w rests
+          const float alpha = !grow ? 1.f : (m == -INFINITY ? 0.f : tc::ex2(m - mx));
+          if (grow) {
+            l *= alpha;
+            m = mx;
+          }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t r[16];
+            tc::tmem_ld16p(t_o + 16 * c, r);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tc::tmem_st16p(t_o + 16 * c, r);
+          }
+          tc::tmem_wait_st();
+        }
+      }
+      const float mref = (m == -INFINITY) ? 0.f : m;
+      const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nm2 = f2(-mref, -mref);
+      uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+#pragma unroll
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int c = 16 * ch + e;  // key pair 2c, 2c + 1
+          float x0, x1;
+          f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), sc2, nm2), x0, x1);
+          const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);  // 2^-inf = 0 on hidden keys
+          if (e & 1) acc1 = add2(acc1, f2(p0, p1));
+          else acc0 = add2(acc0, f2(p0, p1));
+          pk[e] = pack_bf16(p0, p1);
+        }
+        tc::tmem_st16p(t_s + 16 * ch, pk);
+      }
+      {
+        float r0, r1;
+        f2_split(add2(acc0, acc1), r0, r1);
+        l += r0 + r1;
+      }
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&bars[B_PFULL + w]);
+    }
+    const bool live = w == 0 || live_1;
+    if (ok && nw > 0) ok = tc::wait_warp(&bars[B_ODONE + w], 0, abort_flag, wait_ns);
+    if (ok && live) {
+      tc::fence_after_sync();
+      const int head = pair_heads ? h0 + w : h0;
+      const bool mine = my_row < seq.nq;
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
+      if (lse != nullptr && mine)
+        lse[static_cast<size_t>(seq.q0 + my_row) * p.H + head] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      // O / l as bf16 into this warp's 32 rows of the (now free) Q tile, then whole rows out
+      unsigned char* otile = smem + S::kQ + w * S::kTileBytes;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (nw > 0) {
+          tc::tmem_ld32(t_o + 32 * c, r);
+          tc::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+#pragma unroll
+        for (int q8 = 0; q8 < 4; ++q8) {
+          uint32_t v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[e] = pack_bf16(__uint_as_float(r[8 * q8 + 2 * e]) * inv, __uint_as_float(r[8 * q8 + 2 * e + 1]) * inv);
+          const int ch = 4 * c + q8;
+          *reinterpret_cast<uint4*>(otile + (ch / 8) * (kTile * 128) + sw(row, ch % 8)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      __syncwarp();
+      constexpr int kLanes = D / 8;         // lanes that carry a row
+      constexpr int kRows = 32 / kLanes;    // rows per instruction
+      const int ch = lane % kLanes;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kRows) {
+        const int r = 32 * quarter + i + lane / kLanes;
+        if (tile_row + r < seq.nq) {
+          const uint4 v = *reinterpret_cast<const uint4*>(otile + (ch / 8) * (kTile * 128) + sw(r, ch % 8));
+          *reinterpret_cast<uint4*>(o + static_cast<size_t>(seq.q0 + tile_row + r) * p.ld_o + head * D + 8 * ch) = v;
+        }
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) report_status(status, kStatusTimeout);
+  if (warp == 2) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// [rows, heads, d] bf16, rows `ld` elements apart, as (d, heads, rows); box = 64 channels x 128 rows of one head.
+bool make_map(CUtensorMap* map, const void* base, int d, int heads, int rows, long long ld) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {64, 1, kTile};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t run(const Prompt& p, const uint16_t* q, const uint16_t* k, const uint16_t* v, const int32_t* seq_q,
+                const int32_t* seq_k, uint16_t* o, float* lse, unsigned* status, cudaStream_t stream) {
+  if (encode_fn() == nullptr) return cudaErrorNotSupported;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, q, D, p.H, p.rows_q, p.ld_q) || !make_map(&mk, k, D, p.H_kv, p.rows_k, p.ld_k) ||
+      !make_map(&mv, v, D, p.H_kv, p.rows_k, p.ld_v))
+    return cudaErrorInvalidValue;
+  const int smem = Smem<D>::kTotal + 1024;
+  cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // setmaxnreg.inc waits until the block's registers can serve it: refuse a build that would leave it short
+  static int regs = -1;
+  if (regs < 0) {
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, prompt_attn_kernel<D>);
+    if (e != cudaSuccess) return e;
+    regs = attr.numRegs;
+  }
+  if (regs * kThreads < kRegsLow * 128 + kRegsHigh * 256) return cudaErrorInvalidConfiguration;
+  const int pair_heads = (p.H / p.H_kv) % 2 == 0 ? 1 : 0;
+  const int R = pair_heads ? kTile : 2 * kTile;
+  const long long tiles = static_cast<long long>(p.rows_q) / R + p.n_seq;  // at least the sequences' row tiles
+  const long long blocks = tiles * (pair_heads ? p.H / 2 : p.H);
+  prompt_attn_kernel<D><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
+      mq, mk, mv, p, pair_heads, seq_q, seq_k, o, lse, status, attention_wait_limit());
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attn(const Prompt& p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                               const int32_t* seq_q, const int32_t* seq_k, uint16_t* o, float* lse, unsigned* status,
+                               cudaStream_t stream) {
+  if (p.d == 128) return run<128>(p, q, k, v, seq_q, seq_k, o, lse, status, stream);
+  if (p.d == 64) return run<64>(p, q, k, v, seq_q, seq_k, o, lse, status, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sda

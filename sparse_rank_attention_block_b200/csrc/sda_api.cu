@@ -11,6 +11,7 @@
 #include "../../include/sda.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "serving.h"
 
 using sda::Layout;
 using sda::Problem;
@@ -204,6 +205,14 @@ int32_t check_device() {
   if (checked[dev] != 1) return fail(SDA_ERR_DEVICE, "device %d is not sm_100 (the kernels are built for sm_100a)", dev);
   return SDA_OK;
 }
+
+}  // namespace
+
+namespace sda {
+int32_t require_device() { return check_device(); }
+}  // namespace sda
+
+namespace {
 
 int32_t launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(SDA_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));

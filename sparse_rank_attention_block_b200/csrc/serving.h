@@ -1,0 +1,64 @@
+// Internal declarations of the serving operators: prompt attention and the
+// 8-bit key/value cache (host side).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace sda {
+
+// sda_api.cu: checks shared by the entry points.
+int32_t require_device();  // the current device is sm_100 (SDA_ERR_DEVICE otherwise)
+
+// Packed prompts, by value to the kernel.
+struct Prompt {
+  int n_seq, rows_q, rows_k, H, H_kv, d, causal;
+  long long ld_q, ld_k, ld_v, ld_o;  // elements between rows
+  float scale_log2;                  // softmax scale * log2(e)
+};
+
+// prompt_attn_tc.cu
+// Waits keep the limit of sda_set_attention_wait_limit_ns (attention_wait_limit).
+uint64_t attention_wait_limit();
+cudaError_t launch_prompt_attn(const Prompt& p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                               const int32_t* seq_q, const int32_t* seq_k, uint16_t* o, float* lse, unsigned* status,
+                               cudaStream_t stream);
+
+// The cache and its sequences, by value to the kernels.
+struct Cache {
+  int B, H, H_kv, d, block, n_blocks, max_blocks, rows, max_new, weights, keep, recent;
+  int dst_blocks;                    // ceil(keep / block): width of the eviction's target table
+  long long ld_q, ld_k, ld_v, ld_o;
+  float scale_log2;
+};
+
+// Workspace regions of the cache calls (byte offsets).
+struct CacheLayout {
+  size_t status;                     // unsigned status word
+  size_t part_o;                     // [B, H_kv, n_split, row slots, d] fp32 partial outputs
+  size_t part_ml;                    // [B, H_kv, n_split, row slots, 2] fp32 running maximum and sum
+  size_t scores;                     // [B, H_kv, max tokens, row slots] fp32 scores (weights kept only)
+  size_t total;
+  int n_split;                       // pieces of a sequence's tokens
+  int row_tiles;                     // tiles of 16 (query, head) rows of one key head
+  int rows_pad;                      // row slots per key head
+};
+CacheLayout make_cache_layout(const Cache& c);
+
+// cache.cu
+cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_t* v, const int32_t* seq,
+                                const int32_t* lens, const int32_t* table, uint8_t* k_codes, uint8_t* v_codes,
+                                float* k_scale, float* v_scale, float* w, unsigned* status, cudaStream_t stream);
+cudaError_t launch_cache_evict(const Cache& c, const int32_t* lens, const int32_t* table, uint8_t* k_codes,
+                               uint8_t* v_codes, float* k_scale, float* v_scale, float* w, const int32_t* dst_table,
+                               int32_t* kept, int32_t* dst_lens, unsigned* status, cudaStream_t stream);
+
+// cache_attn.cu
+cudaError_t launch_cache_attn(const Cache& c, const CacheLayout& y, void* ws, const uint16_t* q, const int32_t* seq,
+                              const int32_t* lens, const int32_t* table, const uint8_t* k_codes,
+                              const uint8_t* v_codes, const float* k_scale, const float* v_scale, const float* w_in,
+                              float* w_out, uint16_t* o, cudaStream_t stream);
+
+}  // namespace sda

@@ -29,6 +29,8 @@ ERRORS = {-1: "SDA_ERR_NULLPTR", -2: "SDA_ERR_ALIGN", -3: "SDA_ERR_SHAPE", -4: "
 EXPORTS = ["sda_keep_count", "sda_query_blocks", "sda_workspace_size", "sda_workspace_init", "sda_read_status", "sda_block_select",
            "sda_sparse_attn_fwd", "sda_lowrank_fwd", "sda_backward", "sda_backward_workspace_size", "sda_lowrank_fwd_static", "sda_gate_fuse", "sda_qk_prologue", "sda_quant_fp8",
            "sda_forward", "sda_forward_profiled",
+           "sda_prompt_workspace_size", "sda_prompt_attn_fwd", "sda_cache_workspace_size", "sda_cache_append",
+           "sda_cache_attn_fwd", "sda_cache_evict",
            "sda_forward_host_buffer_size", "sda_forward_host", "sda_set_attention_wait_limit_ns",
            "sda_error_string", "sda_last_error_detail", "sda_version"]
 
@@ -51,6 +53,38 @@ def params_of(w: Workload) -> SdaParams:
                      rms_eps=w.rms_eps, gate_per_head=w.gate_per_head, causal_frames=w.causal_frames)
 
 
+class SdaPromptParams(ctypes.Structure):
+    """Mirror of `sda_prompt_params` (include/sda.h)."""
+
+    _fields_ = [("n_seq", ctypes.c_int32), ("rows_q", ctypes.c_int32), ("rows_k", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_o", ctypes.c_int64),
+                ("scale", ctypes.c_double)]
+
+
+class SdaCacheParams(ctypes.Structure):
+    """Mirror of `sda_cache_params` (include/sda.h)."""
+
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_new", ctypes.c_int32), ("weights", ctypes.c_int32),
+                ("keep", ctypes.c_int32), ("recent", ctypes.c_int32), ("ld_q", ctypes.c_int64),
+                ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_o", ctypes.c_int64), ("scale", ctypes.c_double)]
+
+
+def prompt_params(*, n_seq, rows_q, rows_k, H, H_kv, d, causal=True, ld_q=0, ld_k=0, ld_v=0, ld_o=0,
+                  scale=0.0) -> SdaPromptParams:
+    return SdaPromptParams(n_seq=n_seq, rows_q=rows_q, rows_k=rows_k, H=H, H_kv=H_kv, d=d, causal=int(causal),
+                           ld_q=ld_q, ld_k=ld_k, ld_v=ld_v, ld_o=ld_o, scale=scale)
+
+
+def cache_params(*, B, H, H_kv, d, block, n_blocks, max_blocks, rows=0, max_new=0, weights=False, keep=0, recent=0,
+                 ld_q=0, ld_k=0, ld_v=0, ld_o=0, scale=0.0) -> SdaCacheParams:
+    return SdaCacheParams(B=B, H=H, H_kv=H_kv, d=d, block=block, n_blocks=n_blocks, max_blocks=max_blocks, rows=rows,
+                          max_new=max_new, weights=int(weights), keep=keep, recent=recent, ld_q=ld_q, ld_k=ld_k,
+                          ld_v=ld_v, ld_o=ld_o, scale=scale)
+
+
 class SdaError(RuntimeError):
     def __init__(self, code: int, where: str, detail: str):
         super().__init__(f"{where}: {ERRORS.get(code, code)}: {detail}")
@@ -70,6 +104,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
         pp = ctypes.POINTER(SdaParams)
+        pr, pc = ctypes.POINTER(SdaPromptParams), ctypes.POINTER(SdaCacheParams)
         sig = {
             "sda_keep_count": (i32, [pp]),
             "sda_query_blocks": (i32, [pp]),
@@ -87,6 +122,12 @@ def lib() -> ctypes.CDLL:
             "sda_qk_prologue": (i32, [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "sda_forward": (i32, [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "sda_forward_profiled": (i32, [pp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, ctypes.POINTER(vp), vp]),
+            "sda_prompt_workspace_size": (sz, [pr]),
+            "sda_prompt_attn_fwd": (i32, [pr] + [vp] * 8 + [sz, vp]),
+            "sda_cache_workspace_size": (sz, [pc]),
+            "sda_cache_append": (i32, [pc] + [vp] * 11 + [sz, vp]),
+            "sda_cache_attn_fwd": (i32, [pc] + [vp] * 12 + [sz, vp]),
+            "sda_cache_evict": (i32, [pc] + [vp] * 11 + [sz, vp]),
             "sda_forward_host_buffer_size": (sz, [pp]),
             "sda_forward_host": (i32, [pp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "sda_set_attention_wait_limit_ns": (ctypes.c_uint64, [ctypes.c_uint64]),
@@ -212,6 +253,135 @@ def sda_forward_profiled(p, q, k, v, p_q, p_k, g, o, block_idx_out, ws, nbytes, 
            "sda_forward_profiled")
 
 
+# ---------------------------------------------------------------------------
+# serving operators: tensors are checked against the parameters (raw pointers are taken as they are)
+# ---------------------------------------------------------------------------
+
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+
+
+def _refuse(where: str, what: str, code: int = -3):
+    raise SdaError(code, where, what)
+
+
+def _dense(where, dev, t, name, dtype, numel):
+    """Pointer of a dense tensor of this type and size on device number `dev`.
+
+    These checks run on every call of a decoding step, so each is one cheap
+    property of the tensor; the shape itself does not matter to the library."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not dtype or t.nbytes != numel * dtype.itemsize or not t.is_contiguous():
+        _refuse(where, f"{name} must be a dense {dtype} tensor of {numel} elements "
+                       f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()})")
+    if t.get_device() != dev:
+        _refuse(where, f"{name} is on {t.device}, not on cuda:{dev}", -8)
+    return t.data_ptr()
+
+
+def _rows(where, dev, t, name, rows, heads, d, ld):
+    """Pointer of a bf16 [rows, heads, d] tensor whose rows lie ld elements apart (0: dense)."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not _BF16 or t.shape != (rows, heads, d) or \
+            not (t.is_contiguous() if ld == 0 or ld == heads * d else t.stride() == (ld, d, 1)):
+        _refuse(where, f"{name} must be a bfloat16 tensor of shape {(rows, heads, d)} with rows {ld or heads * d} apart "
+                       f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()})")
+    if t.get_device() != dev:
+        _refuse(where, f"{name} is on {t.device}, not on cuda:{dev}", -8)
+    return t.data_ptr()
+
+
+def _device_of(where, *tensors):
+    """Number of the GPU of the first tensor given; None where all are raw pointers."""
+    for t in tensors:
+        if t is not None and type(t) is not int:
+            return t.get_device()
+    return None
+
+
+def _call(name, dev, p, ptrs, ws, nbytes, stream):
+    """The C call on GPU number `dev` and, without a stream, on its current one."""
+    if dev is not None and dev < 0:
+        _refuse(name, "the tensors are not on a GPU", -8)
+    fn = getattr(_lib or lib(), name)
+    if dev is None or dev == torch.cuda.current_device():
+        rc = fn(p, *ptrs, _ptr(ws), nbytes, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(p, *ptrs, _ptr(ws), nbytes, _stream(stream))
+    _check(rc, name)
+
+
+def sda_prompt_workspace_size(p: SdaPromptParams) -> int:
+    n = lib().sda_prompt_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise SdaError(-3, "sda_prompt_workspace_size", lib().sda_last_error_detail().decode())
+    return n
+
+
+def sda_cache_workspace_size(p: SdaCacheParams) -> int:
+    n = lib().sda_cache_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise SdaError(-3, "sda_cache_workspace_size", lib().sda_last_error_detail().decode())
+    return n
+
+
+def sda_prompt_attn_fwd(p: SdaPromptParams, q, k, v, seq_q, seq_k, o, lse, ws, nbytes, stream=None) -> None:
+    f = "sda_prompt_attn_fwd"
+    dev = _device_of(f, q, k, v, o)
+    _call(f, dev, p, (_rows(f, dev, q, "q", p.rows_q, p.H, p.d, p.ld_q),
+                      _rows(f, dev, k, "k", p.rows_k, p.H_kv, p.d, p.ld_k),
+                      _rows(f, dev, v, "v", p.rows_k, p.H_kv, p.d, p.ld_v),
+                      _dense(f, dev, seq_q, "seq_q", _I32, p.n_seq + 1),
+                      _dense(f, dev, seq_k, "seq_k", _I32, p.n_seq + 1),
+                      _rows(f, dev, o, "o", p.rows_q, p.H, p.d, p.ld_o),
+                      _dense(f, dev, lse, "lse", _F32, p.rows_q * p.H)), ws, nbytes, stream)
+
+
+def _pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale):
+    scales = p.n_blocks * p.H_kv
+    codes = scales * p.block * p.d
+    return (_dense(f, dev, lens, "lens", _I32, p.B),
+            _dense(f, dev, block_table, "block_table", _I32, p.B * p.max_blocks),
+            _dense(f, dev, k_codes, "k_codes", _U8, codes), _dense(f, dev, v_codes, "v_codes", _U8, codes),
+            _dense(f, dev, k_scale, "k_scale", _F32, scales), _dense(f, dev, v_scale, "v_scale", _F32, scales))
+
+
+def sda_cache_append(p: SdaCacheParams, k, v, seq, lens, block_table, k_codes, v_codes, k_scale, v_scale, w, ws, nbytes,
+                     stream=None) -> None:
+    f = "sda_cache_append"
+    dev = _device_of(f, k, v, k_codes)
+    _call(f, dev, p, (_rows(f, dev, k, "k", p.rows, p.H_kv, p.d, p.ld_k),
+                      _rows(f, dev, v, "v", p.rows, p.H_kv, p.d, p.ld_v),
+                      _dense(f, dev, seq, "seq", _I32, p.B + 1),
+                      *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
+                      _dense(f, dev, w, "w", _F32, p.n_blocks * p.H_kv * p.block)), ws, nbytes, stream)
+
+
+def sda_cache_attn_fwd(p: SdaCacheParams, q, seq, lens, block_table, k_codes, v_codes, k_scale, v_scale, w_in, w_out, o,
+                       ws, nbytes, stream=None) -> None:
+    f = "sda_cache_attn_fwd"
+    dev = _device_of(f, q, o, k_codes)
+    slots = p.n_blocks * p.H_kv * p.block
+    _call(f, dev, p, (_rows(f, dev, q, "q", p.rows, p.H, p.d, p.ld_q),
+                      _dense(f, dev, seq, "seq", _I32, p.B + 1),
+                      *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
+                      _dense(f, dev, w_in, "w_in", _F32, slots), _dense(f, dev, w_out, "w_out", _F32, slots),
+                      _rows(f, dev, o, "o", p.rows, p.H, p.d, p.ld_o)), ws, nbytes, stream)
+
+
+def sda_cache_evict(p: SdaCacheParams, lens, block_table, k_codes, v_codes, k_scale, v_scale, w, dst_table, kept,
+                    dst_lens, ws, nbytes, stream=None) -> None:
+    f = "sda_cache_evict"
+    dev = _device_of(f, k_codes, v_codes, w)
+    _call(f, dev, p, (*_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
+                      _dense(f, dev, w, "w", _F32, p.n_blocks * p.H_kv * p.block),
+                      _dense(f, dev, dst_table, "dst_table", _I32, p.B * -(-p.keep // p.block)),
+                      _dense(f, dev, kept, "kept", _I32, p.B * p.H_kv * p.keep),
+                      _dense(f, dev, dst_lens, "dst_lens", _I32, p.B)), ws, nbytes, stream)
+
+
 def sda_forward_host_buffer_size(p: SdaParams) -> int:
     return lib().sda_forward_host_buffer_size(ctypes.byref(p))
 
@@ -237,10 +407,12 @@ def sda_version() -> str:
 # ---------------------------------------------------------------------------
 
 class Workspace:
-    """A caller-owned device workspace (torch allocation) sized for `p`."""
+    """A caller-owned device workspace (torch allocation) sized for `p`
+    (SdaParams, SdaPromptParams or SdaCacheParams)."""
 
-    def __init__(self, p: SdaParams, device=None, stream=None):
-        self.nbytes = sda_workspace_size(p)
+    def __init__(self, p, device=None, stream=None):
+        self.nbytes = (sda_prompt_workspace_size(p) if isinstance(p, SdaPromptParams) else
+                       sda_cache_workspace_size(p) if isinstance(p, SdaCacheParams) else sda_workspace_size(p))
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
