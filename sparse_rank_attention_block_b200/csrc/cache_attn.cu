@@ -4,19 +4,26 @@
 //   s_rj = scale * ks_j (q_r . kc_j),  o_r = sum_j p_rj vs_j vc_j,
 //   p_rj = exp(s_rj) / sum_j' exp(s_rj')
 // with kc, vc the E4M3 codes and ks, vs the scales of token j's block. The rows
-// r of a key head are its new tokens times its query heads, 16 to a tile.
+// r of a key head are its new tokens times its query heads, 8 or 16 to a tile.
 //
 // Bound by memory: 2 d bytes of cache for each token and key head against
-// 4 d flops for each of its rows. So codes are read once (16 rows at a time),
+// 4 d flops for each of its rows. So codes are read once for a tile of rows,
 // converted to fp16 in registers (exact) and multiplied by mma.sync
-// m16n8k16: the tensor work of 16 rows is far below its limit.
+// m16n8k16, with the tokens (S^T = K Q^T) and the channels (O^T = V^T P^T) as
+// its 16 rows and the few query rows as its 8 columns: nothing is padded, and
+// the output takes d / 4 registers for 8 query rows.
 //
-// Work is split over the tokens: a CTA takes one piece of one sequence's
-// tokens for one row tile of a key head; each of its warps walks 32-token
-// tiles on its own, with its own ring of TMA loads, running maximum, sum and
-// output (no barrier between warps), merged at the CTA's end. Pieces are
-// joined by a second kernel, which also turns the scores of the first into the
-// tokens' weights (a probability needs the sum over all pieces).
+// Work is split over the tokens of all sequences as one line: sequence by
+// sequence, in it unit by unit (key heads times row tiles), in that the 32-token
+// tiles in order. Every CTA of the one wave of resident CTAs takes an equal
+// stretch of that line, whatever the sequences' lengths. In a unit its warps
+// take the tiles in turn, each with its own ring of TMA loads and its own running
+// maximum, sum and output (no barrier between warps), merged where the unit or
+// the stretch ends. Where a stretch holds all tiles of a unit the CTA writes the
+// output; where it holds a part, a partial sum, which a second kernel joins in
+// the order of the line. That kernel also turns the scores of the first into
+// the tokens' weights (a probability needs the sum over all tokens). Where no
+// sequence can have more than kWholeTiles tiles, a CTA takes one whole unit.
 //
 // Scales differ from block to block. K's multiplies the scores. V's goes into
 // the exponent: with lv = log2 vs, the operand of P V is 2^(s + lv - mv) <= 1
@@ -27,15 +34,20 @@
 // chosen for the loads: a lane reads 16 contiguous bytes of a token at a time
 // and 8 lanes hit 8 different 16-byte bank groups of the swizzled tile.
 //
+// References move, and the output is rescaled, only when a maximum grows by
+// more than 2^8 (exact: every term shares the reference).
+//
 // Tokens that a row must not see get a score of -inf; V codes of tokens behind
 // the sequence (free slots, holding anything) are cleared before use.
 
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "launch.cuh"
 #include "serving.h"
 #include "tc.cuh"
 
@@ -45,20 +57,27 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 32;       // tokens of a warp's tile
+constexpr int kTok = 32;       // tokens of a tile
 constexpr int kStages = 2;     // tiles in flight per warp
 constexpr int kCtasPerSm = 3;
 constexpr int kSms = 148;
+constexpr int kLeast = 8;      // places of a stretch, at least
+// What a unit costs before its first tile (block numbers, scales, Q, the merge at its end: each a chain of
+// reads), in tiles: places without a tile at its start. attn over 16 sequences of 33 to 6,000 tokens, 4 new
+// tokens each: MEASURE.
+constexpr int kLead = 8;
+constexpr int kWholeTiles = 16;
+constexpr int kMaxSeq = 65536;
 
 template <int D>
 struct Smem {
   static constexpr int kHalf = kTok * D;           // K or V codes of a tile
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kWarps * kStages * kStage;
-  // merge at the end, over the ring: per warp 16 rows of output and (m, l, mv)
-  static constexpr int kMerge = kWarps * 16 * (D + 4) * 4;
+  static constexpr int kMerge = kWarps * 16 * (D + 4) * 4;  // at a unit's end, over the ring: outputs and (m, l, mv)
   static constexpr int kBars = kRing > kMerge ? kRing : kMerge;
   static constexpr int kTotal = kBars + 8 * kWarps * kStages + 16;
+  static_assert(kBars >= kMaxSeq / 32 * 4, "the sums over 32 sequences each fit into the ring before its first load");
 };
 
 struct Args {
@@ -69,13 +88,35 @@ struct Args {
   const float* k_scale;
   const float* v_scale;
   uint16_t* o;
-  float* part_o;   // [B, H_kv, n_split, rows_pad, d]
-  float* part_ml;  // [B, H_kv, n_split, rows_pad, 4]: m, l, mv
-  float* scores;   // [B, H_kv, tokens, rows_pad], log2 units; NULL: weights are not kept
+  float* part_o;       // [2 * workers, tile_rows, d]: partial outputs
+  float4* part_ml;     // [2 * workers, tile_rows]: their m, l, mv
+  int* line;           // [B + 1]: where each sequence begins on the line; the last: its length
+  float* lse2;         // [rows, H], log2 of the sum: rows that one stretch holds whole (weights kept)
+  float* scores;       // [B, H_kv, tokens, rows_pad], log2 units; NULL: weights are not kept
   unsigned* status;
-  int n_split, row_tiles, rows_pad;
+  int workers, tile_rows, rows_pad;
+  int whole_row_tiles;  // > 0: CTA i takes unit i, sequences having that many row tiles of room; no line
   uint64_t wait_ns;
 };
+
+// Places of a CTA's stretch of a line of W: CTA i takes [i S, (i + 1) S).
+__device__ __forceinline__ int stretch_size(int W, int workers) { return max(kLeast, (W + workers - 1) / workers); }
+
+// Sequence b on the line: units (row tiles x key heads) of kLead + n_tiles places each. A sequence with rows
+// has one tile at least, so that its rows are written. (The host has checked that the line fits an int.)
+struct SeqLine {
+  NewRows nr;
+  int rows, row_tiles, n_tiles;
+  __device__ __forceinline__ int places(const Cache& c) const { return c.H_kv * row_tiles * (kLead + n_tiles); }
+};
+__device__ __forceinline__ SeqLine seq_line(const Cache& c, const Args& a, int b, bool& bad) {
+  SeqLine s;
+  s.nr = new_rows(c, a.seq, a.lens, b, bad);
+  s.rows = s.nr.n * c.g;
+  s.row_tiles = (s.rows + a.tile_rows - 1) >> (a.tile_rows == 8 ? 3 : 4);  // 8 or 16
+  s.n_tiles = max(1, (s.nr.len + kTok - 1) / kTok);
+  return s;
+}
 
 // Order of the 8 tokens of an n-tile and of the 8 channel groups of a row
 // (d = 128: rows of 8 16-byte chunks): neighbours differ in the bit that the
@@ -99,9 +140,22 @@ __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+// Over the 8 lanes that share lane % 4: the tokens of a column of S^T.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+// Transpose of an 8 x 8 matrix of 16-bit values held as an MMA fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -112,12 +166,13 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
   else return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
-template <int D>
+// NR: groups of 8 query rows. HALVES: a tile's two 16-token halves may lie in different blocks (block = 16).
+template <int D, int NR, bool HALVES>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, Cache c, Args a) {
   using S = Smem<D>;
   constexpr int KS = D / 16;     // k16 steps of a score
-  constexpr int NT = D / 8;      // n-tiles of the output
+  constexpr int MT = D / 16;     // 16-channel tiles of the output
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
@@ -125,473 +180,761 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kStages);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g4 = lane >> 2, cq = lane & 3;
+  const int g = c.g;
 
-  // piece slowest: the empty pieces of short sequences come last
-  const int per_piece = c.B * c.H_kv * a.row_tiles;
-  const int piece = blockIdx.x / per_piece;
-  const int rest = blockIdx.x % per_piece;
-  const int rt = rest % a.row_tiles;
-  const int hk = (rest / a.row_tiles) % c.H_kv;
-  const int b = rest / (a.row_tiles * c.H_kv);
-  const int g = c.H / c.H_kv;
-
-  bool bad = false;
-  const NewRows nr = new_rows(c, a.seq, a.lens, b, bad);
-  if (bad && threadIdx.x == 0) report_status(a.status, kStatusBadIndex);
-  const int rows = nr.n * g;          // rows of this sequence and key head
-  const int r0 = rt * 16;
-  if (r0 >= rows) return;
-  // tokens seen by row r: below first + r / g + 1, and no more than the table holds
-  const int last_row = min(r0 + 15, rows - 1);
-  const int seen = min(nr.len, max(0, nr.first + last_row / g + 1));
-  const int n_tiles = (seen + kTok - 1) / kTok;
-  const int tile0 = static_cast<int>(static_cast<long long>(n_tiles) * piece / a.n_split);
-  const int tile1 = static_cast<int>(static_cast<long long>(n_tiles) * (piece + 1) / a.n_split);
-  const bool whole = a.n_split == 1;
-  const size_t part = (static_cast<size_t>(b) * c.H_kv + hk) * a.n_split + piece;
-  if (tile0 >= tile1 && !whole) {     // nothing in this piece: an empty sum
-    if (threadIdx.x < 16 && r0 + threadIdx.x < rows)
-      *reinterpret_cast<float4*>(a.part_ml + (part * a.rows_pad + r0 + threadIdx.x) * 4) =
-          make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    return;
-  }
   if (threadIdx.x < kWarps * kStages) tc::mbar_init(&bars[threadIdx.x], 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   tc::fence_mbar_init();
-  __syncthreads();
+  pdl_wait();
 
-  const int32_t* blocks = a.table + static_cast<size_t>(b) * c.max_blocks;
+  // ------------------------------------------------------------ this CTA's stretch of the line
+  bool bad = false;
+  int b = 0, unit = 0, tile = 0;
+  int pos = 0, end = 0;  // places on the line: of the next tile, and of the stretch's end
+  SeqLine sl;
+  if (a.whole_row_tiles > 0) {
+    const int per_seq = c.H_kv * a.whole_row_tiles, u = blockIdx.x % per_seq;
+    b = blockIdx.x / per_seq;
+    sl = seq_line(c, a, b, bad);
+    if (bad && threadIdx.x == 0 && u == 0) report_status(a.status, kStatusBadIndex);
+    unit = u / a.whole_row_tiles * sl.row_tiles + u % a.whole_row_tiles;
+    end = u % a.whole_row_tiles < sl.row_tiles ? sl.n_tiles : 0;
+    __syncthreads();
+  } else {
+    int* sums = reinterpret_cast<int*>(smem);  // places of 32 sequences each (the ring is not in use yet)
+    const int groups = (c.B + 31) / 32;
+    for (int u = warp; u < groups; u += kWarps) {
+      const int i = 32 * u + lane;
+      const int n = __reduce_add_sync(0xffffffffu, i < c.B ? seq_line(c, a, i, bad).places(c) : 0);
+      if (lane == 0) sums[u] = n;
+    }
+    if (blockIdx.x == 0 && bad) report_status(a.status, kStatusBadIndex);
+    __syncthreads();
+    int W = 0;
+    for (int u = lane; u < groups; u += 32) W += sums[u];
+    W = __reduce_add_sync(0xffffffffu, W);
+    const int S_ = stretch_size(W, a.workers);
+    pos = min(static_cast<long long>(blockIdx.x) * S_, static_cast<long long>(W));
+    end = min(static_cast<long long>(pos) + S_, static_cast<long long>(W));
+    // the group of sequences that holds pos, then the sequence: `before` is where it begins
+    int before = 0;
+    auto find = [&](int n) {  // lane that holds pos among the lanes' n places each, -1: behind them
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const uint32_t at = __ballot_sync(0xffffffffu, pos >= before + incl - n && pos < before + incl);
+      const int found = __ffs(at) - 1;
+      before += found >= 0 ? __shfl_sync(0xffffffffu, incl - n, found) : __shfl_sync(0xffffffffu, incl, 31);
+      return found;
+    };
+    int group = 0;
+    for (int base = 0; base < groups; base += 32) {
+      const int at = find(base + lane < groups ? sums[base + lane] : 0);
+      if (at >= 0) {
+        group = base + at;
+        break;
+      }
+    }
+    const int at = find(32 * group + lane < c.B ? seq_line(c, a, 32 * group + lane, bad).places(c) : 0);
+    if (at >= 0) b = 32 * group + at;
+    if (blockIdx.x == 0) {  // the line for the second kernel
+      int start = 0;
+      for (int u = 0; u < groups; ++u) {
+        if (u % kWarps == warp) {
+          const int n = 32 * u + lane < c.B ? seq_line(c, a, 32 * u + lane, bad).places(c) : 0;
+          int incl = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          if (32 * u + lane < c.B) a.line[32 * u + lane] = start + incl - n;
+        }
+        start += sums[u];
+      }
+      if (threadIdx.x == 0) a.line[c.B] = W;
+    }
+    tc::fence_proxy_async_smem();
+    __syncthreads();  // the sums have been read: the ring may be filled
+    sl = seq_line(c, a, b, bad);
+    if (pos < end) {
+      unit = (pos - before) / (kLead + sl.n_tiles);
+      tile = (pos - before) % (kLead + sl.n_tiles) - kLead;
+      if (tile < 0) {     // on the places before the unit's first tile
+        pos -= tile;
+        tile = 0;
+      }
+    }
+  }
+  pdl_launch();
+
+  // codes are read once (and again by a unit's other row tiles, soon after): L2 is for the scores
+  const uint64_t once = tc::l2_evict_first();
   const int shift = 31 - __clz(c.block);
   unsigned char* ring = smem + warp * kStages * S::kStage;
   uint64_t* full = bars + warp * kStages;
-
-  // block of a 16-token half tile, -1 where the number is not one of the pool
-  auto block_of = [&](int t16) {
-    const int tok = t16 * 16;
-    if (tok >= seen) return -1;
-    const int blk = __ldg(blocks + (tok >> shift));
-    return blk >= 0 && blk < c.n_blocks ? blk : -1;
-  };
-  const int my_tiles = tile1 - tile0 > warp ? (tile1 - tile0 - warp + kWarps - 1) / kWarps : 0;
-  // This warp's blocks and scales, a batch of 16 tiles per register: lane l holds half l % 2 of tile
-  // base + l / 2. The next batch is read a batch ahead of its use.
-  struct Held {
-    int blk;
-    float ks, vs;
-  };
-  auto hold = [&](int base) {
-    Held x{-1, 0.f, 0.f};
-    const int i = base + lane / 2;
-    if (i < my_tiles) {
-      const int t = tile0 + warp + i * kWarps;
-      x.blk = block_of(t * 2 + (lane & 1));
-      if (x.blk < 0 && t * kTok + 16 * (lane & 1) < seen) report_status(a.status, kStatusBadIndex);
-      if (x.blk >= 0) {
-        const size_t head = static_cast<size_t>(x.blk) * c.H_kv + hk;
-        x.ks = __ldg(a.k_scale + head);
-        x.vs = __ldg(a.v_scale + head);
-      }
-    }
-    return x;
-  };
-  // one lane: the loads of tile i into its stage (absent blocks: nothing, their tokens are not seen)
-  auto load_tile = [&](int i, int blk0, int blk1) {
-    const int st = i % kStages;
-    const int tok = (tile0 + warp + i * kWarps) * kTok;
-    unsigned char* dst = ring + st * S::kStage;
-    if (c.block >= kTok) {
-      tc::mbar_arrive_expect_tx(&full[st], blk0 >= 0 ? S::kStage : 0);
-      if (blk0 >= 0) {
-        const int y = (blk0 * c.H_kv + hk) * c.block + (tok & (c.block - 1));
-        tc::tma_load_2d(dst, &tm_k, &full[st], 0, y);
-        tc::tma_load_2d(dst + S::kHalf, &tm_v, &full[st], 0, y);
-      }
-    } else {
-      tc::mbar_arrive_expect_tx(&full[st], (blk0 >= 0 ? S::kHalf : 0) + (blk1 >= 0 ? S::kHalf : 0));
-      for (int u = 0; u < 2; ++u) {
-        const int blk = u ? blk1 : blk0;
-        if (blk < 0) continue;
-        const int y = (blk * c.H_kv + hk) * c.block;
-        tc::tma_load_2d(dst + u * 16 * D, &tm_k, &full[st], 0, y);
-        tc::tma_load_2d(dst + S::kHalf + u * 16 * D, &tm_v, &full[st], 0, y);
-      }
-    }
-  };
-
-  Held now = hold(0);
-  int issued = 0;
-  for (; issued < kStages && issued < my_tiles; ++issued) {
-    const int b0 = __shfl_sync(0xffffffffu, now.blk, 2 * issued), b1 = __shfl_sync(0xffffffffu, now.blk, 2 * issued + 1);
-    if (lane == 0) load_tile(issued, b0, b1);
-  }
-  Held next = hold(16);
-
-  // Q fragments in fp16: row r times 2^(14 - e), e its exponent, undone in the score's factor
-  uint32_t qf[KS][4];
-  float factor[2];
-  int lim[2];                         // tokens that rows g4 and g4 + 8 of the tile see
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int r = r0 + g4 + 8 * u;
-    const bool there = r < rows;
-    const int i = there ? r / g : 0, qh = there ? r % g : 0;
-    lim[u] = there ? min(nr.len, max(0, nr.first + i + 1)) : seen;  // rows that are not there: computed, not kept
-    const uint16_t* src = a.q + static_cast<size_t>(nr.row0 + i) * c.ld_q + (hk * g + qh) * D;
-    uint4 x[D / 32];                  // this lane's channels: 16 at 16 cq (and 16 at 64 + 16 cq)
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e)
-      x[e] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * (e / 2) + 16 * cq + 8 * (e % 2)))
-                   : make_uint4(0u, 0u, 0u, 0u);
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-      for (int f = 0; f < 4; ++f) top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[f])), fabsf(bf16_hi(in[f]))));
-    }
-    top = quad_max(top);
-    const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
-    const float up = __uint_as_float(static_cast<uint32_t>(14 - e2 + 127) << 23);
-    factor[u] = __uint_as_float(static_cast<uint32_t>(e2 - 14 + 127) << 23) * c.scale_log2;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) {
-      const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {   // channels 8 e' + 2 f, + 1 of the lane's 16
-        const int kk = 4 * (e / 2) + 2 * (e % 2) + f / 2;
-        qf[kk][u + 2 * (f % 2)] = pack_f16(bf16_lo(in[f]) * up, bf16_hi(in[f]) * up);
-      }
-    }
-  }
-
-  float acc[NT][4];
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float* my_scores = a.scores == nullptr
-                         ? nullptr
-                         : a.scores + (static_cast<size_t>(b) * c.H_kv + hk) * c.max_blocks * c.block * a.rows_pad;
+  int done = 0;       // tiles of this warp so far: their places in the ring go on from segment to segment
   bool ok = true;
 
-  for (int i = 0; i < my_tiles; ++i) {
-    const int st = i % kStages;
-    const int tok0 = (tile0 + warp + i * kWarps) * kTok;
-    if (i % 16 == 0 && i > 0) {
-      now = next;
-      next = hold(i + 16);
-    }
-    const int la = 2 * (i % 16), lb = la + 1;
-    const int blk_a = __shfl_sync(0xffffffffu, now.blk, la), blk_b = __shfl_sync(0xffffffffu, now.blk, lb);
-    const float ks_a = __shfl_sync(0xffffffffu, now.ks, la), ks_b = __shfl_sync(0xffffffffu, now.ks, lb);
-    const float vs_a = __shfl_sync(0xffffffffu, now.vs, la), vs_b = __shfl_sync(0xffffffffu, now.vs, lb);
-    ok = tc::wait_warp(&full[st], (i / kStages) & 1, abort_flag, a.wait_ns);
-    if (!ok) break;
-    const unsigned char* kt = ring + st * S::kStage;
-    const unsigned char* vt = kt + S::kHalf;
+  while (pos < end) {
+    // ---------------------------------------------------------- a segment: tiles [tile, tile + seg_all) of one unit
+    const int hk = unit / sl.row_tiles, r0 = 8 * NR * (unit % sl.row_tiles);
+    const int seg_all = min(sl.n_tiles - tile, end - pos);
+    // this warp's tiles: tile0 + kWarps i, i < seg
+    const int tile0 = tile + warp, seg = seg_all > warp ? (seg_all - warp + kWarps - 1) / kWarps : 0;
+    // tokens that the tile's last row sees
+    const int seen = min(sl.nr.len, max(0, sl.nr.first + min(r0 + 8 * NR - 1, sl.rows - 1) / g + 1));
+    const int32_t* blocks = a.table + static_cast<size_t>(b) * c.max_blocks;
 
-    // scores of the 32 tokens: n-tile n holds tokens 8 n + order(2 cq), 8 n + order(2 cq + 1) of this lane
-    float s[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int row = 8 * n + (D == 128 ? spread(g4) : g4);
-      s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-#pragma unroll
-      for (int half = 0; half < KS / 4; ++half) {
-        const uint4 x = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(row, cq + 4 * half));
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_f16(s[n], qf[4 * half + e], e4m3x2_to_f16x2(static_cast<uint16_t>(in[e])),
-                  e4m3x2_to_f16x2(static_cast<uint16_t>(in[e] >> 16)));
-      }
-    }
-    const int t_lo = D == 128 ? cq : 2 * cq, t_hi = D == 128 ? cq + 4 : 2 * cq + 1;  // the lane's tokens of an n-tile
-    const bool edge = tok0 + kTok > min(lim[0], lim[1]) || blk_a < 0 || blk_b < 0;
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] *= factor[e / 2] * (n < 2 ? ks_a : ks_b);
-    if (__any_sync(0xffffffffu, edge)) {
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = tok0 + 8 * n + (e % 2 ? t_hi : t_lo);
-          if (tok >= lim[e / 2] || (n < 2 ? blk_a : blk_b) < 0) s[n][e] = -INFINITY;
+    // This segment's blocks and scales, a batch of 16 tiles per register: lane l holds half l % 2 of tile
+    // base + l / 2. The next batch is read a batch ahead of its use.
+    struct Held {
+      int blk;
+      float ks, vs;
+    };
+    auto hold = [&](int base) {
+      Held x{-1, 0.f, 0.f};
+      const int i = base + lane / 2, tok = (tile0 + kWarps * i) * kTok + 16 * (lane & 1);
+      if (i < seg && tok < seen) {
+        x.blk = __ldg(blocks + (tok >> shift));
+        if (x.blk < 0 || x.blk >= c.n_blocks) {
+          report_status(a.status, kStatusBadIndex);
+          x.blk = -1;
+        } else {
+          const size_t head = static_cast<size_t>(x.blk) * c.H_kv + hk;
+          x.ks = __ldg(a.k_scale + head);
+          x.vs = __ldg(a.v_scale + head);
         }
+      }
+      return x;
+    };
+    // one lane: the loads of the segment's tile i (absent blocks: nothing, their tokens are not seen)
+    auto load_tile = [&](int i, int blk0, int blk1) {
+      const int st = (done + i) % kStages;
+      const int tok = (tile0 + kWarps * i) * kTok;
+      unsigned char* dst = ring + st * S::kStage;
+      if constexpr (!HALVES) {
+        tc::mbar_arrive_expect_tx(&full[st], blk0 >= 0 ? S::kStage : 0);
+        if (blk0 >= 0) {
+          const int y = (blk0 * c.H_kv + hk) * c.block + (tok & (c.block - 1));
+          tc::tma_load_2d(dst, &tm_k, &full[st], 0, y, once);
+          tc::tma_load_2d(dst + S::kHalf, &tm_v, &full[st], 0, y, once);
+        }
+      } else {
+        tc::mbar_arrive_expect_tx(&full[st], (blk0 >= 0 ? S::kHalf : 0) + (blk1 >= 0 ? S::kHalf : 0));
+        for (int u = 0; u < 2; ++u) {
+          const int blk = u ? blk1 : blk0;
+          if (blk < 0) continue;
+          const int y = (blk * c.H_kv + hk) * c.block;
+          tc::tma_load_2d(dst + u * 16 * D, &tm_k, &full[st], 0, y, once);
+          tc::tma_load_2d(dst + S::kHalf + u * 16 * D, &tm_v, &full[st], 0, y, once);
+        }
+      }
+    };
+    Held now = hold(0);
+    int issued = 0;
+    for (; issued < kStages && issued < seg; ++issued) {
+      const int b0 = __shfl_sync(0xffffffffu, now.blk, 2 * issued), b1 = __shfl_sync(0xffffffffu, now.blk, 2 * issued + 1);
+      if (lane == 0) load_tile(issued, b0, b1);
     }
-    if (my_scores != nullptr) {
+    Held next = hold(16);
+
+    // Q fragments in fp16: row r times 2^(14 - e), e its exponent, undone in the score's factor
+    uint32_t qf[NR][KS][2];
+    float factor[NR][2];              // of this lane's columns: rows 2 cq and 2 cq + 1 of each group of 8
+    int lim[NR][2];                   // tokens that they see
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = r0 + 8 * nr + g4;
+      const bool there = r < sl.rows;
+      const int i = there ? r / g : 0, qh = there ? r % g : 0;
+      const int my_lim = there ? min(sl.nr.len, max(0, sl.nr.first + i + 1)) : seen;  // rows not there: computed, not kept
+      const uint16_t* src = a.q + static_cast<size_t>(sl.nr.row0 + i) * c.ld_q + (hk * g + qh) * D;
+      uint4 x[D / 32];                // this lane's channels: 16 at 16 cq (and 16 at 64 + 16 cq)
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        x[e] = there ? __ldg(reinterpret_cast<const uint4*>(src + 64 * (e / 2) + 16 * cq + 8 * (e % 2)))
+                     : make_uint4(0u, 0u, 0u, 0u);
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f) top = fmaxf(top, fmaxf(fabsf(bf16_lo(in[f])), fabsf(bf16_hi(in[f]))));
+      }
+      top = quad_max(top);
+      const int e2 = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e2 + 127) << 23);
+      const float my_factor = __uint_as_float(static_cast<uint32_t>(e2 - 14 + 127) << 23) * c.scale_log2;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) {
+        const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+        for (int f = 0; f < 4; ++f)   // channels 8 e' + 2 f, + 1 of the lane's 16
+          qf[nr][4 * (e / 2) + 2 * (e % 2) + f / 2][f % 2] = pack_f16(bf16_lo(in[f]) * up, bf16_hi(in[f]) * up);
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int r = r0 + g4 + 8 * u;
-        if (r < rows) {
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int tok = tok0 + 8 * n + (e ? t_hi : t_lo);
-              if (tok < seen) my_scores[static_cast<size_t>(tok) * a.rows_pad + r] = s[n][2 * u + e];
-            }
-        }
+        factor[nr][u] = __shfl_sync(0xffffffffu, my_factor, 4 * (2 * cq + u));
+        lim[nr][u] = __shfl_sync(0xffffffffu, my_lim, 4 * (2 * cq + u));
       }
     }
-    // running maxima; lv = log2 of V's scale
-    const float lv_a = __log2f(vs_a), lv_b = __log2f(vs_b);
-    uint32_t pf[2][4];                // P fragments of the two k16 steps
-    float alpha_v[2];
+    int lim_least = lim[0][0];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float ma = quad_max(fmaxf(fmaxf(s[0][2 * u], s[0][2 * u + 1]), fmaxf(s[1][2 * u], s[1][2 * u + 1])));
-      const float mb = quad_max(fmaxf(fmaxf(s[2][2 * u], s[2][2 * u + 1]), fmaxf(s[3][2 * u], s[3][2 * u + 1])));
-      const float m_new = fmaxf(m[u], fmaxf(ma, mb));
-      const float mv_new = fmaxf(mv[u], fmaxf(ma + lv_a, mb + lv_b));
-      const float mr = finite_or_0(m_new), mvr = finite_or_0(mv_new);
-      l[u] *= tc::ex2(m[u] - mr);
-      alpha_v[u] = tc::ex2(mv[u] - mvr);
-      m[u] = m_new;
-      mv[u] = mv_new;
-      // 2^(s + lv - mv) = 2^(s - m) 2^(m + lv - mv)
-      const float fa = tc::ex2(fminf(mr + lv_a - mvr, 127.f)), fb = tc::ex2(fminf(mr + lv_b - mvr, 127.f));
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float p0 = tc::ex2(s[n][2 * u] - mr), p1 = tc::ex2(s[n][2 * u + 1] - mr);
-        sum += p0 + p1;
-        const float f = n < 2 ? fa : fb;
-        pf[n / 2][u + 2 * (n % 2)] = pack_f16(p0 * f, p1 * f);
-      }
-      l[u] += sum;
-    }
-    if (__any_sync(0xffffffffu, alpha_v[0] != 1.f || alpha_v[1] != 1.f)) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][e] *= alpha_v[e / 2];
-    }
-    // O += P V: this lane's n-tiles j are its channel group g4, its tokens those of P
-    const bool clear = tok0 + kTok > seen || blk_a < 0 || blk_b < 0;  // V rows of no token of the sequence
-#pragma unroll
-    for (int n2 = 0; n2 < 2; ++n2) {
-      uint32_t w[4][D / 32];          // 4 tokens, d / 8 channels of the lane's group
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * n2 + 8 * (e / 2) + (e % 2 ? t_hi : t_lo);
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(row, spread(g4)));
-          w[e][0] = x.x;
-          w[e][1] = x.y;
-          w[e][2] = x.z;
-          w[e][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(row, g4 >> 1) + 8 * (g4 & 1));
-          w[e][0] = x.x;
-          w[e][1] = x.y;
-        }
-        if (clear && (tok0 + row >= seen || (n2 == 0 ? blk_a : blk_b) < 0)) {
-#pragma unroll
-          for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < D / 32; ++f) {
-        // channels 4 f .. 4 f + 3 of the group, tokens paired byte by byte
-        const uint32_t a01 = __byte_perm(w[0][f], w[1][f], 0x5140), a23 = __byte_perm(w[0][f], w[1][f], 0x7362);
-        const uint32_t b01 = __byte_perm(w[2][f], w[3][f], 0x5140), b23 = __byte_perm(w[2][f], w[3][f], 0x7362);
-        mma_f16(acc[4 * f], pf[n2], e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01)));
-        mma_f16(acc[4 * f + 1], pf[n2], e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16)));
-        mma_f16(acc[4 * f + 2], pf[n2], e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23)));
-        mma_f16(acc[4 * f + 3], pf[n2], e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16)));
-      }
-    }
-    __syncwarp();                     // every lane has read the stage
-    if (issued < my_tiles) {
-      const int from = issued / 16 == i / 16 ? now.blk : next.blk;
-      const int b0 = __shfl_sync(0xffffffffu, from, 2 * (issued % 16)), b1 = __shfl_sync(0xffffffffu, from, 2 * (issued % 16) + 1);
-      if (lane == 0) load_tile(issued, b0, b1);
-      ++issued;
-    }
-  }
-  if (!ok) {                          // given up: no load is in flight when the CTA ends
-    volatile int never = 0;
-    for (int i = max(0, issued - kStages); i < issued; ++i) tc::wait_warp(&full[i % kStages], (i / kStages) & 1, &never);
-  }
+    for (int nr = 0; nr < NR; ++nr) lim_least = min(lim_least, min(lim[nr][0], lim[nr][1]));
 
-  // ---------------------------------------------------------------- merge of the warps
-  __syncthreads();                    // the ring is free
-  if (*abort_flag) {
-    if (threadIdx.x == 0) report_status(a.status, kStatusTimeout);
-    return;
-  }
-  float* mo = reinterpret_cast<float*>(smem);                 // [warp][16][D + 4]: a row's output, then (m, l, mv)
-  constexpr int LD = D + 4;
+    float acc[NR][MT][4];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    l[u] = quad_sum(l[u]);
-    float* row = mo + (warp * 16 + g4 + 8 * u) * LD;
+    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      // n index 2 cq and 2 cq + 1 of n-tile j: channel j of their groups
-      const int grp0 = D == 128 ? cq : 2 * cq, grp1 = D == 128 ? cq + 4 : 2 * cq + 1;
-      row[(D / 8) * grp0 + j] = acc[j][2 * u];
-      row[(D / 8) * grp1 + j] = acc[j][2 * u + 1];
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nr][j][e] = 0.f;
+    float m[NR][2], mv[NR][2], l[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m[nr][u] = mv[nr][u] = -INFINITY;
+        l[nr][u] = 0.f;
+      }
+    float* my_scores = a.scores == nullptr ? nullptr
+                                           : a.scores +
+                                                 (static_cast<size_t>(b) * c.H_kv + hk) * c.max_blocks * c.block * a.rows_pad +
+                                                 r0 + 2 * cq;
+    // the MMA's row i stands for token (D == 128: spread(i)) of each 8
+    const int row_k = D == 128 ? spread(g4) : g4;
+    const int t_lo = D == 128 ? cq : 2 * cq, t_hi = D == 128 ? cq + 4 : 2 * cq + 1;  // the tokens of MMA rows 2 cq, 2 cq + 1
+
+    for (int i = 0; i < seg; ++i) {
+      const int st = (done + i) % kStages;
+      const int tok0 = (tile0 + kWarps * i) * kTok;
+      if (i % 16 == 0 && i > 0) {
+        now = next;
+        next = hold(i + 16);
+      }
+      int blk[2];
+      float ks[2], lv[2];             // lv = log2 of V's scale
+#pragma unroll
+      for (int hf = 0; hf < (HALVES ? 2 : 1); ++hf) {
+        const int from = 2 * (i % 16) + hf;
+        blk[hf] = __shfl_sync(0xffffffffu, now.blk, from);
+        ks[hf] = __shfl_sync(0xffffffffu, now.ks, from);
+        lv[hf] = __log2f(__shfl_sync(0xffffffffu, now.vs, from));
+      }
+      if constexpr (!HALVES) {
+        blk[1] = blk[0];
+        ks[1] = ks[0];
+        lv[1] = lv[0];
+      }
+      ok = tc::wait_warp(&full[st], ((done + i) / kStages) & 1, abort_flag, a.wait_ns);
+      if (!ok) break;                 // the load stays counted as issued
+      const unsigned char* kt = ring + st * S::kStage;
+      const unsigned char* vt = kt + S::kHalf;
+
+      // S^T of the 32 tokens: s[hf]: tokens 16 hf + row_k (e < 2) and 16 hf + 8 + row_k, columns 2 cq + e % 2
+      float s[NR][2][4];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) s[nr][hf][0] = s[nr][hf][1] = s[nr][hf][2] = s[nr][hf][3] = 0.f;
+#pragma unroll
+        for (int half = 0; half < KS / 4; ++half) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(16 * hf + row_k, cq + 4 * half));
+          const uint4 y = *reinterpret_cast<const uint4*>(kt + chunk_at<D>(16 * hf + 8 + row_k, cq + 4 * half));
+          const uint32_t in_x[4] = {x.x, x.y, x.z, x.w}, in_y[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t kf[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(in_x[e])),
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(in_y[e])),
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(in_x[e] >> 16)),
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(in_y[e] >> 16))};
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16(s[nr][hf], kf, qf[nr][4 * half + e][0], qf[nr][4 * half + e][1]);
+          }
+        }
+      }
+      const bool edge = tok0 + kTok > lim_least || blk[0] < 0 || blk[1] < 0;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float f0 = factor[nr][u] * ks[0], f1 = factor[nr][u] * ks[1];
+          s[nr][0][u] *= f0;
+          s[nr][0][2 + u] *= f0;
+          s[nr][1][u] *= f1;
+          s[nr][1][2 + u] *= f1;
+        }
+      if (__any_sync(0xffffffffu, edge)) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (tok0 + 16 * hf + 8 * (e / 2) + row_k >= lim[nr][e % 2] || blk[hf] < 0) s[nr][hf][e] = -INFINITY;
+      }
+      if (my_scores != nullptr) {     // two rows at a time; the second may be a free slot
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+          if (r0 + 8 * nr + 2 * cq < sl.rows) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int tok = tok0 + 16 * hf + 8 * e + row_k;
+                if (tok < seen)
+                  *reinterpret_cast<float2*>(my_scores + static_cast<size_t>(tok) * a.rows_pad + 8 * nr) =
+                      make_float2(s[nr][hf][2 * e], s[nr][hf][2 * e + 1]);
+              }
+          }
+      }
+      float top[NR][2], top_v[NR][2];
+      bool grow = false;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (HALVES) {
+            const float ma = column_max(fmaxf(s[nr][0][u], s[nr][0][2 + u]));
+            const float mb = column_max(fmaxf(s[nr][1][u], s[nr][1][2 + u]));
+            top[nr][u] = fmaxf(ma, mb);
+            top_v[nr][u] = fmaxf(ma + lv[0], mb + lv[1]);
+          } else {
+            top[nr][u] = column_max(fmaxf(fmaxf(s[nr][0][u], s[nr][0][2 + u]), fmaxf(s[nr][1][u], s[nr][1][2 + u])));
+            top_v[nr][u] = top[nr][u] + lv[0];
+          }
+          grow = grow || top[nr][u] > m[nr][u] + 8.f || top_v[nr][u] > mv[nr][u] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float m_new = fmaxf(m[nr][u], top[nr][u]), mv_new = fmaxf(mv[nr][u], top_v[nr][u]);
+            l[nr][u] *= tc::ex2(m[nr][u] - finite_or_0(m_new));
+            const float alpha = tc::ex2(mv[nr][u] - finite_or_0(mv_new));
+            m[nr][u] = m_new;
+            mv[nr][u] = mv_new;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              acc[nr][j][u] *= alpha;
+              acc[nr][j][2 + u] *= alpha;
+            }
+          }
+      }
+      uint32_t pf[NR][2][2];          // P^T fragments of the two 16-token steps
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        float p[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float mr = finite_or_0(m[nr][u]), mvr = finite_or_0(mv[nr][u]);
+          // 2^(s + lv - mv) = 2^(s - m) 2^(m + lv - mv)
+          const float fa = tc::ex2(fminf(mr + lv[0] - mvr, 127.f));
+          const float fb = HALVES ? tc::ex2(fminf(mr + lv[1] - mvr, 127.f)) : fa;
+          const float a0 = tc::ex2(s[nr][0][u] - mr), a1 = tc::ex2(s[nr][0][2 + u] - mr);
+          const float b0 = tc::ex2(s[nr][1][u] - mr), b1 = tc::ex2(s[nr][1][2 + u] - mr);
+          l[nr][u] += (a0 + a1) + (b0 + b1);
+          p[0][u] = a0 * fa;
+          p[0][2 + u] = a1 * fa;
+          p[1][u] = b0 * fb;
+          p[1][2 + u] = b1 * fb;
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          pf[nr][hf][0] = transpose8(pack_f16(p[hf][0], p[hf][1]));
+          pf[nr][hf][1] = transpose8(pack_f16(p[hf][2], p[hf][3]));
+        }
+      }
+      // O^T += V^T P^T: this lane's channels are those of group g4, two to an MMA; its tokens those of P
+      const bool clear = tok0 + kTok > seen || blk[0] < 0 || blk[1] < 0;  // V rows of no token of the sequence
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t w[4][D / 32];        // 4 tokens, d / 8 channels of the lane's group
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * hf + 8 * (e / 2) + (e % 2 ? t_hi : t_lo);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(row, spread(g4)));
+            w[e][0] = x.x;
+            w[e][1] = x.y;
+            w[e][2] = x.z;
+            w[e][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(row, g4 >> 1) + 8 * (g4 & 1));
+            w[e][0] = x.x;
+            w[e][1] = x.y;
+          }
+          if (clear && (tok0 + row >= seen || blk[hf] < 0)) {
+#pragma unroll
+            for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+          // channels 4 f .. 4 f + 3 of the group, tokens paired byte by byte
+          const uint32_t a01 = __byte_perm(w[0][f], w[1][f], 0x5140), a23 = __byte_perm(w[0][f], w[1][f], 0x7362);
+          const uint32_t b01 = __byte_perm(w[2][f], w[3][f], 0x5140), b23 = __byte_perm(w[2][f], w[3][f], 0x7362);
+          const uint32_t v0[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
+                                  e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))};
+          const uint32_t v1[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
+                                  e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))};
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            mma_f16(acc[nr][2 * f], v0, pf[nr][hf][0], pf[nr][hf][1]);
+            mma_f16(acc[nr][2 * f + 1], v1, pf[nr][hf][0], pf[nr][hf][1]);
+          }
+        }
+      }
+      __syncwarp();                   // every lane has read the stage
+      if (issued < seg) {
+        const int from = issued / 16 == i / 16 ? now.blk : next.blk;
+        const int b0 = __shfl_sync(0xffffffffu, from, 2 * (issued % 16)), b1 = __shfl_sync(0xffffffffu, from, 2 * (issued % 16) + 1);
+        if (lane == 0) load_tile(issued, b0, b1);
+        ++issued;
+      }
     }
-    if (cq == 0) {
-      row[D] = m[u];
-      row[D + 1] = l[u];
-      row[D + 2] = mv[u];
+    if (!ok) {                        // given up: no load is in flight when the CTA ends
+      volatile int never = 0;
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        tc::wait_warp(&full[(done + i) % kStages], ((done + i) / kStages) & 1, &never);
+    }
+    done += seg;
+
+    // ---------------------------------------------------------- the warps' outputs merged
+    constexpr int LD = D + 4, ROWS = 8 * NR;
+    float* merge = reinterpret_cast<float*>(smem);              // [warp][ROWS][LD]: a row's output, then (m, l, mv)
+    __syncthreads();                                            // the ring is free
+    if (*abort_flag) break;                                     // uniform
+    const int ch0 = D == 128 ? 16 * spread(g4) : 8 * g4;        // this lane's channels: d / 8 from here
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float L = column_sum(l[nr][u]);
+        float* row = merge + (warp * ROWS + 8 * nr + 2 * cq + u) * LD;
+#pragma unroll
+        for (int j = 0; j < MT; j += 2)
+          *reinterpret_cast<float4*>(row + ch0 + 2 * j) =
+              make_float4(acc[nr][j][u], acc[nr][j][2 + u], acc[nr][j + 1][u], acc[nr][j + 1][2 + u]);
+        if (g4 == 0) *reinterpret_cast<float4*>(row + D) = make_float4(m[nr][u], L, mv[nr][u], 0.f);
+      }
+    __syncthreads();
+    {
+      constexpr int PER = kThreads / ROWS;                      // threads of a row, 4 channels each at a time
+      const int r = threadIdx.x / PER, t = threadIdx.x % PER, rr = r0 + r;
+      if (rr < sl.rows) {
+        float4 st[kWarps];
+        float M = -INFINITY, MV = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) {
+          st[u] = *reinterpret_cast<const float4*>(merge + (u * ROWS + r) * LD + D);
+          M = fmaxf(M, st[u].x);
+          MV = fmaxf(MV, st[u].z);
+        }
+        const float Mr = finite_or_0(M), MVr = finite_or_0(MV);
+        float L = 0.f, f[kWarps];
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) {
+          L = fmaf(st[u].y, tc::ex2(st[u].x - Mr), L);
+          f[u] = tc::ex2(st[u].z - MVr);
+        }
+        const bool whole = tile == 0 && seg_all == sl.n_tiles;
+        const int row = sl.nr.row0 + rr / g, head = hk * g + rr % g;
+        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (tile == 0 ? 1 : 0)) * ROWS + r;  // a unit's first part, or a later one
+        const float fin = L > 0.f ? tc::ex2(MVr - Mr) / L : (L == 0.f ? 0.f : L);
+        if (t == 0) {
+          if (!whole) a.part_ml[slot] = make_float4(M, L, MV, 0.f);
+          else if (a.scores != nullptr) a.lse2[static_cast<size_t>(row) * c.H + head] = M == -INFINITY ? INFINITY : M + log2f(L);
+        }
+#pragma unroll
+        for (int ch = 4 * t; ch < D; ch += 4 * PER) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < kWarps; ++u) {
+            const float4 y = *reinterpret_cast<const float4*>(merge + (u * ROWS + r) * LD + ch);
+            x.x = fmaf(y.x, f[u], x.x);
+            x.y = fmaf(y.y, f[u], x.y);
+            x.z = fmaf(y.z, f[u], x.z);
+            x.w = fmaf(y.w, f[u], x.w);
+          }
+          if (whole)
+            *reinterpret_cast<uint2*>(a.o + static_cast<size_t>(row) * c.ld_o + head * D + ch) =
+                make_uint2(pack_bf16(x.x * fin, x.y * fin), pack_bf16(x.z * fin, x.w * fin));
+          else
+            *reinterpret_cast<float4*>(a.part_o + slot * D + ch) = x;
+        }
+      }
+    }
+    // ---------------------------------------------------------- the next unit
+    pos += seg_all + kLead;
+    tile = 0;
+    if (pos < end) {
+      tc::fence_proxy_async_smem();
+      __syncthreads();                // the merge has been read: the ring may be filled
+      if (++unit >= c.H_kv * sl.row_tiles) {
+        unit = 0;
+        do {
+          sl = seq_line(c, a, ++b, bad);
+        } while (sl.rows == 0);
+      }
     }
   }
-  __syncthreads();
-  // 8 threads a row
-  const int r = threadIdx.x / 8, part8 = threadIdx.x % 8;
-  if (r0 + r >= rows) return;
-  float M = -INFINITY, MV = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < kWarps; ++u) {
-    M = fmaxf(M, mo[(u * 16 + r) * LD + D]);
-    MV = fmaxf(MV, mo[(u * 16 + r) * LD + D + 2]);
-  }
-  const float Mr = finite_or_0(M), MVr = finite_or_0(MV);
-  float L = 0.f, fac[kWarps];
-#pragma unroll
-  for (int u = 0; u < kWarps; ++u) {
-    L += mo[(u * 16 + r) * LD + D + 1] * tc::ex2(mo[(u * 16 + r) * LD + D] - Mr);
-    fac[u] = tc::ex2(mo[(u * 16 + r) * LD + D + 2] - MVr);
-  }
-  const float fin = L > 0.f ? tc::ex2(MVr - Mr) / L : (L == 0.f ? 0.f : L);
-  const size_t prow = part * a.rows_pad + r0 + r;
-  if ((!whole || a.scores != nullptr) && part8 == 0) *reinterpret_cast<float4*>(a.part_ml + prow * 4) = make_float4(M, L, MV, 0.f);
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) {  // 4 channels at a time, 8 threads side by side
-    const int ch = 32 * e + 4 * part8;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < kWarps; ++u) {
-      const float4 y = *reinterpret_cast<const float4*>(mo + (u * 16 + r) * LD + ch);
-      x.x = fmaf(y.x, fac[u], x.x);
-      x.y = fmaf(y.y, fac[u], x.y);
-      x.z = fmaf(y.z, fac[u], x.z);
-      x.w = fmaf(y.w, fac[u], x.w);
-    }
-    if (whole) {
-      const int rr = r0 + r;
-      uint16_t* dst = a.o + static_cast<size_t>(nr.row0 + rr / g) * c.ld_o + (hk * g + rr % g) * D + ch;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x * fin, x.y * fin), pack_bf16(x.z * fin, x.w * fin));
-    } else {
-      *reinterpret_cast<float4*>(a.part_o + prow * D + ch) = x;
-    }
-  }
+  if (*abort_flag && threadIdx.x == 0) report_status(a.status, kStatusTimeout);
 }
 
 // ---------------------------------------------------------------------------
-// second kernel: the pieces' outputs joined, and the weights. CTAs
-// [0, n_join) join 8 rows each (a warp per row); the others take kSpan tokens
-// of one sequence and key head.
+// second kernel: the parts' outputs joined, and each row's sum. Bound by the
+// latency of a few dependent reads.
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinThreads = 256;
-constexpr int kSpan = 1024;
-constexpr int kMaxRowsHeld = 1024;
+constexpr int kMaxParts = kSms * kCtasPerSm;
 
-template <int D>
+// The slots of a unit's parts: 2 first + 1, then 2 (first + 1), 2 (first + 2) .. 2 last.
+struct Parts {
+  int first, n;
+  __device__ __forceinline__ size_t slot(int i) const { return 2 * static_cast<size_t>(first + i) + (i == 0 ? 1 : 0); }
+};
+// Of a unit that begins at place `start` of a line of stretches of `size` places.
+__device__ __forceinline__ Parts parts_of(int start, int n_tiles, int size) {
+  const int first = (start + kLead) / size;
+  return Parts{first, (start + kLead + n_tiles - 1) / size - first + 1};
+}
+
+// WIDE: a CTA per row (many parts); otherwise a warp per row.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads)
-cache_join_kernel(Cache c, Args a, int n_join, int row_groups, int spans, const float* w_in, float* w_out) {
-  __shared__ float lse2[kMaxRowsHeld];
-  const int g = c.H / c.H_kv;
+cache_join_kernel(Cache c, Args a) {
+  constexpr int V = D / 32;      // channels of a lane
+  constexpr int NW = kJoinThreads / 32;
+  const int g = c.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   bool bad = false;
-  if (static_cast<int>(blockIdx.x) < n_join) {
-    const int rg = blockIdx.x % row_groups, hk = (blockIdx.x / row_groups) % c.H_kv, b = blockIdx.x / (row_groups * c.H_kv);
-    const NewRows nr = new_rows(c, a.seq, a.lens, b, bad);
-    const int r = rg * 8 + warp;
-    if (r >= nr.n * g) return;
-    const size_t part0 = (static_cast<size_t>(b) * c.H_kv + hk) * a.n_split;
+  pdl_wait();
+  pdl_launch();
+  const int size = stretch_size(a.line[c.B], a.workers);
+  auto keep_sum = [&](const SeqLine& sl, int hk, int r, float M, float L) {
+    if (a.scores != nullptr)
+      a.lse2[static_cast<size_t>(sl.nr.row0 + r / g) * c.H + hk * g + r % g] = M == -INFINITY ? INFINITY : M + log2f(L);
+  };
+  if constexpr (!WIDE) {
+    const int id = blockIdx.x * NW + warp;
+    const int r = id % a.rows_pad, hk = (id / a.rows_pad) % c.H_kv, b = id / (a.rows_pad * c.H_kv);
+    if (b >= c.B) return;
+    const SeqLine sl = seq_line(c, a, b, bad);
+    if (r >= sl.rows) return;
+    const Parts ps =
+        parts_of(a.line[b] + (hk * sl.row_tiles + r / a.tile_rows) * (kLead + sl.n_tiles), sl.n_tiles, size);
+    const int n = ps.n, r_in = r % a.tile_rows;
+    if (n == 1) return;          // written by the first kernel
+    float M = -INFINITY, MV = -INFINITY, L = 0.f, x[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const float4 st = i0 + lane < n ? a.part_ml[ps.slot(i0 + lane) * a.tile_rows + r_in]
+                                      : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      float Mn = st.x, MVn = st.z;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+        MVn = fmaxf(MVn, __shfl_xor_sync(0xffffffffu, MVn, o));
+      }
+      Mn = fmaxf(M, Mn);
+      MVn = fmaxf(MV, MVn);
+      const float Mr = finite_or_0(Mn), MVr = finite_or_0(MVn);
+      L = L * tc::ex2(M - Mr) + warp_sum(st.y * tc::ex2(st.x - Mr));
+      const float f0 = tc::ex2(MV - MVr), f = tc::ex2(st.z - MVr);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[e] *= f0;
+      M = Mn;
+      MV = MVn;
+      const int m = min(32, n - i0);
+#pragma unroll 8
+      for (int i = 0; i < m; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* po = a.part_o + (ps.slot(i0 + i) * a.tile_rows + r_in) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[e] = fmaf(po[e], fi, x[e]);  // one 8- or 16-byte read
+      }
+    }
+    const float fin = L > 0.f ? tc::ex2(finite_or_0(MV) - finite_or_0(M)) / L : (L == 0.f ? 0.f : L);
+    uint16_t* dst = a.o + static_cast<size_t>(sl.nr.row0 + r / g) * c.ld_o + (hk * g + r % g) * D + lane * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0] * fin, x[1] * fin), pack_bf16(x[2] * fin, x[3] * fin));
+    else *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x[0] * fin, x[1] * fin);
+    if (lane == 0) keep_sum(sl, hk, r, M, L);
+  } else {
+    __shared__ float held[kMaxParts];
+    __shared__ float part[NW][D];
+    __shared__ float red[3][NW];
+    const int r = blockIdx.x % a.rows_pad, hk = (blockIdx.x / a.rows_pad) % c.H_kv, b = blockIdx.x / (a.rows_pad * c.H_kv);
+    const SeqLine sl = seq_line(c, a, b, bad);
+    if (r >= sl.rows) return;
+    const Parts ps =
+        parts_of(a.line[b] + (hk * sl.row_tiles + r / a.tile_rows) * (kLead + sl.n_tiles), sl.n_tiles, size);
+    const int n = ps.n, r_in = r % a.tile_rows;
+    if (n == 1) return;          // written by the first kernel
     float M = -INFINITY, MV = -INFINITY;
-    for (int s = lane; s < a.n_split; s += 32) {
-      const float4 x = *reinterpret_cast<const float4*>(a.part_ml + ((part0 + s) * a.rows_pad + r) * 4);
-      M = fmaxf(M, x.x);
-      MV = fmaxf(MV, x.z);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+      const float4 st = a.part_ml[ps.slot(i) * a.tile_rows + r_in];
+      M = fmaxf(M, st.x);
+      MV = fmaxf(MV, st.z);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       MV = fmaxf(MV, __shfl_xor_sync(0xffffffffu, MV, o));
     }
-    const float Mr = finite_or_0(M), MVr = finite_or_0(MV);
-    float L = 0.f, x[D / 32];
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) x[e] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.n_split; ++s) {
-      const float4 st = *reinterpret_cast<const float4*>(a.part_ml + ((part0 + s) * a.rows_pad + r) * 4);
-      if (st.x == -INFINITY) continue;  // an empty piece wrote no output
-      L = fmaf(st.y, tc::ex2(st.x - Mr), L);
-      const float f = tc::ex2(st.z - MVr);
-      const float* po = a.part_o + ((part0 + s) * a.rows_pad + r) * D;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) x[e] = fmaf(po[lane * (D / 32) + e], f, x[e]);
-    }
-    const float fin = L > 0.f ? tc::ex2(MVr - Mr) / L : (L == 0.f ? 0.f : L);
-    uint16_t* dst = a.o + static_cast<size_t>(nr.row0 + r / g) * c.ld_o + (hk * g + r % g) * D + lane * (D / 32);
-    if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0] * fin, x[1] * fin), pack_bf16(x[2] * fin, x[3] * fin));
-    else *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x[0] * fin, x[1] * fin);
-    return;
-  }
-  const int id = blockIdx.x - n_join;
-  const int sp = id / (c.B * c.H_kv), hk = id % c.H_kv, b = (id / c.H_kv) % c.B;
-  const NewRows nr = new_rows(c, a.seq, a.lens, b, bad);
-  const int rows = nr.n * g;
-  const int tok0 = sp * kSpan, tok1 = min(tok0 + kSpan, nr.len);
-  if (tok0 >= tok1) return;
-  const size_t part0 = (static_cast<size_t>(b) * c.H_kv + hk) * a.n_split;
-  const float* sc = a.scores + (static_cast<size_t>(b) * c.H_kv + hk) * c.max_blocks * c.block * a.rows_pad;
-  float sum[kSpan / kJoinThreads];
-#pragma unroll
-  for (int e = 0; e < kSpan / kJoinThreads; ++e) sum[e] = 0.f;
-  for (int base = 0; base < rows; base += kMaxRowsHeld) {
-    const int n = min(kMaxRowsHeld, rows - base);
-    if (base > 0) __syncthreads();
-    for (int r = warp; r < n; r += kJoinThreads / 32) {  // log2 of the row's sum over all pieces
-      float M = -INFINITY, L = 0.f;
-      for (int s = lane; s < a.n_split; s += 32) {
-        const float4 x = *reinterpret_cast<const float4*>(a.part_ml + ((part0 + s) * a.rows_pad + base + r) * 4);
-        const float Mn = fmaxf(M, x.x);
-        if (Mn != -INFINITY) L = L * tc::ex2(M - Mn) + x.y * tc::ex2(x.x - Mn);
-        M = Mn;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float M2 = __shfl_xor_sync(0xffffffffu, M, o), L2 = __shfl_xor_sync(0xffffffffu, L, o);
-        const float Mn = fmaxf(M, M2);
-        if (Mn != -INFINITY) L = L * tc::ex2(M - Mn) + L2 * tc::ex2(M2 - Mn);
-        M = Mn;
-      }
-      if (lane == 0) lse2[r] = M == -INFINITY ? INFINITY : M + log2f(L);
+    if (lane == 0) {
+      red[0][warp] = M;
+      red[1][warp] = MV;
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kSpan / kJoinThreads; ++e) {
-      const int tok = tok0 + e * kJoinThreads + threadIdx.x;
-      if (tok >= tok1) continue;
-      const float* row = sc + static_cast<size_t>(tok) * a.rows_pad + base;
-      for (int r = 0; r < n; ++r) {
-        // rows that end before this token left no score behind
-        if (tok < min(nr.len, nr.first + (base + r) / g + 1)) sum[e] += tc::ex2(row[r] - lse2[r]);
+    for (int u = 0; u < NW; ++u) {
+      M = fmaxf(M, red[0][u]);
+      MV = fmaxf(MV, red[1][u]);
+    }
+    const float Mr = finite_or_0(M), MVr = finite_or_0(MV);
+    float L = 0.f;
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+      const float4 st = a.part_ml[ps.slot(i) * a.tile_rows + r_in];
+      L = fmaf(st.y, tc::ex2(st.x - Mr), L);
+      held[i] = tc::ex2(st.z - MVr);
+    }
+    L = warp_sum(L);
+    if (lane == 0) red[2][warp] = L;
+    __syncthreads();
+    float x[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = 0.f;
+#pragma unroll 8
+    for (int i = warp; i < n; i += NW) {
+      const float f = held[i];
+      const float* po = a.part_o + (ps.slot(i) * a.tile_rows + r_in) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(po);
+        x[0] = fmaf(y.x, f, x[0]);
+        x[1] = fmaf(y.y, f, x[1]);
+        x[2] = fmaf(y.z, f, x[2]);
+        x[3] = fmaf(y.w, f, x[3]);
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(po);
+        x[0] = fmaf(y.x, f, x[0]);
+        x[1] = fmaf(y.y, f, x[1]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[warp][lane * V + e] = x[e];
+    __syncthreads();
+    if (warp != 0) return;
+    L = 0.f;
+#pragma unroll
+    for (int u = 0; u < NW; ++u) L += red[2][u];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      x[e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < NW; ++u) x[e] += part[u][lane * V + e];
+    }
+    const float fin = L > 0.f ? tc::ex2(MVr - Mr) / L : (L == 0.f ? 0.f : L);
+    uint16_t* dst = a.o + static_cast<size_t>(sl.nr.row0 + r / g) * c.ld_o + (hk * g + r % g) * D + lane * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x[0] * fin, x[1] * fin), pack_bf16(x[2] * fin, x[3] * fin));
+    else *reinterpret_cast<uint32_t*>(dst) = pack_bf16(x[0] * fin, x[1] * fin);
+    if (lane == 0) keep_sum(sl, hk, r, M, L);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// third kernel: the weights, from the scores (most still in L2) and the rows'
+// sums. A thread takes a token, or SIDE threads side by side one token of many
+// rows, four rows each at a time.
+// ---------------------------------------------------------------------------
+
+constexpr int kWeightThreads = 256;
+constexpr int kWeightTokens = 8;    // per thread
+constexpr int kMaxRowsHeld = 512;
+
+template <int SIDE>
+__global__ void __launch_bounds__(kWeightThreads)
+cache_weights_kernel(Cache c, Args a, const float* w_in, float* w_out) {
+  constexpr int T = kWeightTokens, STEP = kWeightThreads / SIDE;
+  __shared__ __align__(16) float held[kMaxRowsHeld];
+  pdl_wait();
+  const int hk = blockIdx.z, b = blockIdx.y, tok0 = blockIdx.x * (T * STEP);
+  bool bad = false;
+  const NewRows nr = new_rows(c, a.seq, a.lens, b, bad);
+  const int tok1 = nr.len, g = c.g, rows = nr.n * g;
+  if (tok0 >= tok1) return;
+  const int shift = 31 - __clz(c.block), q = threadIdx.x % SIDE, t0 = tok0 + threadIdx.x / SIDE;
+  float sum[T];
+#pragma unroll
+  for (int e = 0; e < T; ++e) sum[e] = 0.f;
+  const float* sc = a.scores + (static_cast<size_t>(b) * c.H_kv + hk) * c.max_blocks * c.block * a.rows_pad;
+  for (int base = 0; base < rows; base += kMaxRowsHeld) {
+    const int n = min(kMaxRowsHeld, rows - base), n4 = (n + 3) / 4 * 4;
+    // the first four rows' scores and the rows' sums are on their way together
+    float4 x[T];
+    auto read = [&](int r) {
+#pragma unroll
+      for (int e = 0; e < T; ++e)
+        x[e] = r < n && t0 + e * STEP < tok1
+                   ? __ldcs(reinterpret_cast<const float4*>(sc + static_cast<size_t>(t0 + e * STEP) * a.rows_pad + base + r))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    read(4 * q);
+    if (base > 0) __syncthreads();
+    for (int rr = threadIdx.x; rr < n4; rr += kWeightThreads) {
+      const int r = base + rr;
+      held[rr] = rr < n ? a.lse2[static_cast<size_t>(nr.row0 + r / g) * c.H + hk * g + r % g] : INFINITY;
+    }
+    __syncthreads();
+    const bool all_seen = tok0 + T * STEP <= nr.first + 1 && n % 4 == 0;
+    for (int r = 4 * q; r < n; r += 4 * SIDE) {
+      const float4 h4 = *reinterpret_cast<const float4*>(held + r);
+      if (r >= 4 * SIDE) read(r);
+#pragma unroll
+      for (int e = 0; e < T; ++e) {
+        float p0 = tc::ex2(x[e].x - h4.x), p1 = tc::ex2(x[e].y - h4.y), p2 = tc::ex2(x[e].z - h4.z), p3 = tc::ex2(x[e].w - h4.w);
+        if (!all_seen) {
+          // rows that end before a token left no score for it: the first that sees it is row (tok - first) g
+          const int from = min(max(t0 + e * STEP - nr.first, 0), nr.n) * g - base - r;
+          p0 = from <= 0 ? p0 : 0.f;
+          p1 = from <= 1 && r + 1 < n ? p1 : 0.f;
+          p2 = from <= 2 && r + 2 < n ? p2 : 0.f;
+          p3 = from <= 3 && r + 3 < n ? p3 : 0.f;
+        }
+        sum[e] += (p0 + p1) + (p2 + p3);
       }
     }
   }
-  const int shift = 31 - __clz(c.block);
+  int at[T];                          // the tokens' places in w, -1: none
+  const int32_t* blocks = a.table + static_cast<size_t>(b) * c.max_blocks;
 #pragma unroll
-  for (int e = 0; e < kSpan / kJoinThreads; ++e) {
-    const int tok = tok0 + e * kJoinThreads + threadIdx.x;
-    if (tok >= tok1) continue;
-    const int blk = __ldg(a.table + static_cast<size_t>(b) * c.max_blocks + (tok >> shift));
-    if (blk < 0 || blk >= c.n_blocks) continue;
-    const size_t at = (static_cast<size_t>(blk) * c.H_kv + hk) * c.block + (tok & (c.block - 1));
-    w_out[at] = (w_in != nullptr ? w_in[at] : 0.f) + sum[e];
+  for (int e = 0; e < T; ++e) {
+    const int tok = t0 + e * STEP;
+    at[e] = q == 0 && tok < tok1 ? __ldg(blocks + (tok >> shift)) : -1;
   }
+#pragma unroll
+  for (int e = 0; e < T; ++e) {
+    at[e] = at[e] >= 0 && at[e] < c.n_blocks ? (at[e] * c.H_kv + hk) * c.block + ((t0 + e * STEP) & (c.block - 1)) : -1;
+#pragma unroll
+    for (int o = 1; o < SIDE; o <<= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+  }
+  if (w_in != nullptr) {
+    float old[T];
+#pragma unroll
+    for (int e = 0; e < T; ++e) old[e] = at[e] >= 0 ? w_in[at[e]] : 0.f;
+#pragma unroll
+    for (int e = 0; e < T; ++e) sum[e] += old[e];
+  }
+#pragma unroll
+  for (int e = 0; e < T; ++e)
+    if (at[e] >= 0) w_out[at[e]] = sum[e];
 }
 
 // ---------------------------------------------------------------------------
@@ -626,29 +969,42 @@ bool make_map(CUtensorMap* map, const void* base, const Cache& c) {
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int D, int NR, bool HALVES>
+cudaError_t run_attn(const Cache& c, const Args& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+  const int smem = Smem<D>::kTotal + 1024;
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NR, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_after(cache_attn_kernel<D, NR, HALVES>, dim3(a.workers), dim3(kThreads), smem, stream, mk, mv, c, a);
+}
+
 template <int D>
 cudaError_t run(const Cache& c, const Args& a, const uint8_t* k_codes, const uint8_t* v_codes, const float* w_in,
                 float* w_out, cudaStream_t stream) {
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
   CUtensorMap mk, mv;
   if (!make_map(&mk, k_codes, c) || !make_map(&mv, v_codes, c)) return cudaErrorInvalidValue;
-  const int smem = Smem<D>::kTotal + 1024;
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const bool halves = c.block < kTok, one = a.tile_rows == 8;
+  cudaError_t e = halves ? (one ? run_attn<D, 1, true>(c, a, mk, mv, stream) : run_attn<D, 2, true>(c, a, mk, mv, stream))
+                               : (one ? run_attn<D, 1, false>(c, a, mk, mv, stream) : run_attn<D, 2, false>(c, a, mk, mv, stream));
   if (e != cudaSuccess) return e;
-  const long long heads = static_cast<long long>(c.B) * c.H_kv;
-  const long long blocks = heads * a.row_tiles * a.n_split;
-  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  cache_attn_kernel<D><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(mk, mv, c, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || (a.n_split == 1 && a.scores == nullptr)) return e;
-  const int row_groups = a.rows_pad / 8 + (a.rows_pad % 8 != 0);
-  const long long n_join = a.n_split > 1 ? heads * row_groups : 0;
-  const int spans = a.scores == nullptr ? 0 : (c.max_blocks * c.block + kSpan - 1) / kSpan;
-  const long long all = n_join + heads * spans;
-  if (all >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-  cache_join_kernel<D><<<static_cast<unsigned>(all), kJoinThreads, 0, stream>>>(c, a, static_cast<int>(n_join), row_groups,
-                                                                               spans, w_in, w_out);
-  return cudaGetLastError();
+  if (a.whole_row_tiles == 0) {
+    // A row's parts number about workers / units. A CTA per row costs many rows of few parts several waves, a
+    // warp per row costs few rows of many parts a chain of reads: the CTA from 16 parts on.
+    const int rows = c.B * c.H_kv * a.rows_pad;
+    const bool wide = a.workers >= 16 * c.B * c.H_kv * ((a.rows_pad + a.tile_rows - 1) / a.tile_rows);
+    e = wide ? launch_after(cache_join_kernel<D, true>, dim3(rows), dim3(kJoinThreads), 0, stream, c, a)
+             : launch_after(cache_join_kernel<D, false>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)),
+                            dim3(kJoinThreads), 0, stream, c, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.scores == nullptr) return cudaSuccess;
+  auto weights = [&](auto side) {
+    constexpr int SIDE = decltype(side)::value, SPAN = kWeightTokens * kWeightThreads / SIDE;
+    const int spans = (c.max_blocks * c.block + SPAN - 1) / SPAN;
+    return launch_after(cache_weights_kernel<SIDE>, dim3(spans, c.B, c.H_kv), dim3(kWeightThreads), 0, stream, c, a, w_in,
+                        w_out);
+  };
+  return a.rows_pad >= 16 ? weights(std::integral_constant<int, 4>{}) : weights(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -657,25 +1013,27 @@ CacheLayout make_cache_layout(const Cache& c) {
   CacheLayout y{};
   const long long heads = static_cast<long long>(c.B) * c.H_kv;
   const int most = c.max_new < c.rows ? c.max_new : c.rows;  // rows of one sequence
-  const int rows = (most > 0 ? most : 1) * (c.H / c.H_kv);
-  y.row_tiles = (rows + 15) / 16;
+  const int rows = (most > 0 ? most : 1) * (c.g);
   y.rows_pad = (rows + 3) / 4 * 4;
-  // Pieces: one wave of resident CTAs where the batch leaves room for it, of 512 tokens at least;
-  // for batches above half a wave pieces of 2048 tokens, so that sequences of unequal length spread;
-  // one piece where there are many row tiles.
+  y.tile_rows = rows <= 8 ? 8 : 16;
   const long long tokens = static_cast<long long>(c.max_blocks) * c.block;
-  const long long slots = static_cast<long long>(kSms) * kCtasPerSm, base = heads * y.row_tiles;
-  long long n = base * 2 <= slots ? slots / base : base >= 16 * slots ? 1 : (tokens + 2047) / 2048;
-  const long long most_pieces = (tokens + 511) / 512;
-  if (n > most_pieces) n = most_pieces;
-  y.n_split = static_cast<int>(n < 1 ? 1 : n);
+  // one wave of resident CTAs, or as many as the longest possible line fills
+  const long long row_tiles = (rows + y.tile_rows - 1) / y.tile_rows, most_tiles = (tokens + kTok - 1) / kTok;
+  y.line_places = heads * row_tiles * (kLead + most_tiles);
+  long long ctas = (y.line_places + kLeast - 1) / kLeast;
+  if (ctas > kSms * kCtasPerSm) ctas = kSms * kCtasPerSm;
+  y.whole_row_tiles = most_tiles <= kWholeTiles && heads * row_tiles < (1ll << 31) ? static_cast<int>(row_tiles) : 0;
+  y.workers = static_cast<int>(y.whole_row_tiles > 0 ? heads * row_tiles : ctas);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t off = 256;
-  const size_t slots_rows = static_cast<size_t>(heads) * y.n_split * y.rows_pad;
-  y.part_o = off;   off = up(off + (y.n_split > 1 ? slots_rows * c.d * 4 : 0));
-  y.part_ml = off;  off = up(off + (y.n_split > 1 || c.weights ? slots_rows * 16 : 0));
+  const size_t slots = y.whole_row_tiles > 0 ? 0 : 2 * static_cast<size_t>(y.workers) * y.tile_rows;
+  y.line = off;     off = up(off + (static_cast<size_t>(c.B) + 1) * 4);
+  y.part_o = off;   off = up(off + slots * c.d * 4);
+  y.part_ml = off;  off = up(off + slots * 16);
+  y.lse2 = off;     off = up(off + (c.weights ? static_cast<size_t>(c.rows) * c.H * 4 : 0));
   y.scores = off;   off = up(off + (c.weights ? static_cast<size_t>(heads) * tokens * y.rows_pad * 4 : 0));
   y.total = off;
+  y.join_ctas = heads * y.rows_pad;
   return y;
 }
 
@@ -693,11 +1051,14 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheLayout& y, void* ws, co
   a.v_scale = v_scale;
   a.o = o;
   a.part_o = reinterpret_cast<float*>(base + y.part_o);
-  a.part_ml = reinterpret_cast<float*>(base + y.part_ml);
+  a.part_ml = reinterpret_cast<float4*>(base + y.part_ml);
+  a.line = reinterpret_cast<int*>(base + y.line);
+  a.lse2 = reinterpret_cast<float*>(base + y.lse2);
   a.scores = w_out != nullptr ? reinterpret_cast<float*>(base + y.scores) : nullptr;
   a.status = reinterpret_cast<unsigned*>(base);
-  a.n_split = y.n_split;
-  a.row_tiles = y.row_tiles;
+  a.workers = y.workers;
+  a.tile_rows = y.tile_rows;
+  a.whole_row_tiles = y.whole_row_tiles;
   a.rows_pad = y.rows_pad;
   a.wait_ns = attention_wait_limit();
   if (c.d == 128) return run<128>(c, a, k_codes, v_codes, w_in, w_out, stream);

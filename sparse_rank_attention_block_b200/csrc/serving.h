@@ -29,6 +29,7 @@ cudaError_t launch_prompt_attn(const Prompt& p, const uint16_t* q, const uint16_
 // The cache and its sequences, by value to the kernels.
 struct Cache {
   int B, H, H_kv, d, block, n_blocks, max_blocks, rows, max_new, weights, keep, recent;
+  int g;                             // query heads of a key head
   int dst_blocks;                    // ceil(keep / block): width of the eviction's target table
   long long ld_q, ld_k, ld_v, ld_o;
   float scale_log2;
@@ -37,13 +38,18 @@ struct Cache {
 // Workspace regions of the cache calls (byte offsets).
 struct CacheLayout {
   size_t status;                     // unsigned status word
-  size_t part_o;                     // [B, H_kv, n_split, row slots, d] fp32 partial outputs
-  size_t part_ml;                    // [B, H_kv, n_split, row slots, 2] fp32 running maximum and sum
-  size_t scores;                     // [B, H_kv, max tokens, row slots] fp32 scores (weights kept only)
+  size_t line;                       // [B + 1] int32: the sequences' places in the order of work
+  size_t part_o;                     // [2 * workers, tile_rows, d] fp32 partial outputs
+  size_t part_ml;                    // [2 * workers, tile_rows, 4] fp32: their running maxima and sums
+  size_t lse2;                       // [rows, H] fp32 (weights kept only)
+  size_t scores;                     // [B, H_kv, max tokens, rows_pad] fp32 scores (weights kept only)
   size_t total;
-  int n_split;                       // pieces of a sequence's tokens
-  int row_tiles;                     // tiles of 16 (query, head) rows of one key head
+  int workers;                       // CTAs that share the work
+  int whole_row_tiles;               // > 0: a CTA per unit (short sequences), of so many row tiles per key head
+  int tile_rows;                     // query rows of a tile: 8 or 16
   int rows_pad;                      // row slots per key head
+  long long join_ctas;               // CTAs of the second kernel, at most
+  long long line_places;             // the longest possible line of work
 };
 CacheLayout make_cache_layout(const Cache& c);
 

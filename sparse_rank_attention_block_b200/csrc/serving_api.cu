@@ -124,6 +124,7 @@ int32_t make_cache(const sda_cache_params* p, Cache* C) {
   C->B = p->B;
   C->H = p->H;
   C->H_kv = p->H_kv;
+  C->g = p->H / p->H_kv;
   C->d = p->d;
   C->block = p->block;
   C->n_blocks = p->n_blocks;
@@ -218,6 +219,8 @@ int32_t sda_cache_attn_fwd(const sda_cache_params* p, const uint16_t* q, const i
   SDA_TRY(make_cache(p, &C));
   SDA_TRY(need_rows(C));
   const CacheLayout y = sda::make_cache_layout(C);
+  if (y.join_ctas >= (1ll << 31) || y.line_places >= (1ll << 31) - (1 << 20))
+    return fail(SDA_ERR_UNSUPPORTED, "too much work for one launch (B * H * max_new rows over max_blocks * block tokens)");
   SDA_TRY(check_ws(y.total, ws, ws_bytes));
   SDA_TRY(check_ptr(q, "q"));
   SDA_TRY(check_ptr(seq, "seq"));
