@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "launch.cuh"
 #include "serving.h"
 
 namespace sda {
@@ -43,6 +44,7 @@ __global__ void cache_append_kernel(Cache c, int touched, const uint16_t* __rest
   const int b = blockIdx.y;
   const int is_v = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.H_kv, i = (blockIdx.x >> 1) / c.H_kv;
   bool bad = false;
+  pdl_wait();
   const NewRows r = new_rows(c, seq, lens, b, bad);
   bad = bad || r.first < 0;
   const int start = max(r.first, 0);
@@ -98,12 +100,12 @@ __global__ void cache_append_kernel(Cache c, int touched, const uint16_t* __rest
   if (warps == 1) __syncwarp();
   if (threadIdx.x == 0) *scale = after;
   if (slot0 > 0) {
-    const float ratio = before / after;
-    if (ratio != 1.f)
+    const Rescale again(before / after);
+    if (before != after)
       for (int row = row0; row < slot0; row += step) {
         uint2* at = reinterpret_cast<uint2*>(codes + row * D) + ch;
         const uint2 old = *at;
-        *at = make_uint2(e4m3x4_rescale(old.x, ratio), e4m3x4_rescale(old.y, ratio));
+        *at = make_uint2(again(old.x), again(old.y));
       }
   }
   // x / scale: for a power of two (every scale that append chose) the product with its inverse is the quotient
@@ -144,15 +146,17 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 
 __global__ void __launch_bounds__(kSelThreads)
 cache_select_kernel(Cache c, int cap, const int32_t* __restrict__ lens, const int32_t* __restrict__ table,
-                    const float* __restrict__ w, int32_t* __restrict__ kept, int32_t* __restrict__ dst_lens,
-                    unsigned* status) {
-  extern __shared__ uint32_t keys[];
+                    const float* __restrict__ w, int32_t* __restrict__ kept, int32_t* __restrict__ rows,
+                    int32_t* __restrict__ dst_lens, unsigned* status) {
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[256];
   __shared__ uint32_t found[2];  // digit, tokens above it
   __shared__ int warp_gt[32], warp_eq[32];
   const int h = blockIdx.x % c.H_kv, b = blockIdx.x / c.H_kv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int shift_b = 31 - __clz(c.block);
   const int32_t* blocks = table + static_cast<size_t>(b) * c.max_blocks;
+  pdl_wait();
   const int given = __ldg(lens + b);
   const int len = min(max(given, 0), c.max_blocks * c.block);
   const int n = min(len, c.keep), last = min(c.recent, n);
@@ -161,42 +165,59 @@ cache_select_kernel(Cache c, int cap, const int32_t* __restrict__ lens, const in
     dst_lens[b] = n;
     if (len != given) report_status(status, kStatusBadIndex);
   }
-  auto load_key = [&](int t) -> uint32_t {
-    const int blk = __ldg(blocks + t / c.block);
-    if (blk < 0 || blk >= c.n_blocks) {
-      report_status(status, kStatusBadIndex);
-      return 0u;
-    }
-    return weight_key(__ldg(w + (static_cast<size_t>(blk) * c.H_kv + h) * c.block + t % c.block));
+  // row of the pool that holds token t, -1 where its block is none of the pool's
+  auto row_of = [&](int t) {
+    const int blk = __ldg(blocks + (t >> shift_b));
+    if (blk >= 0 && blk < c.n_blocks) return (blk * c.H_kv + h) * c.block + (t & (c.block - 1));
+    report_status(status, kStatusBadIndex);
+    return -1;
   };
-  int32_t* out = kept + (static_cast<size_t>(b) * c.H_kv + h) * c.keep;
-  for (int t = threadIdx.x; t < c.keep - need; t += kSelThreads) out[need + t] = t < last ? older + t : -1;
+  // keys of tokens t .. t + 3 (t a multiple of 4: one block), 0 in a block that is none of the pool's
+  auto load_keys = [&](int t) {
+    const int row = row_of(t);
+    const float4 x = row >= 0 ? __ldg(reinterpret_cast<const float4*>(w + row)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return row >= 0 ? make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  const size_t out0 = (static_cast<size_t>(b) * c.H_kv + h) * c.keep;
+  auto stay = [&](int i, int t) {
+    kept[out0 + i] = t;
+    if (t >= 0) rows[out0 + i] = row_of(t);
+  };
+  pdl_launch();
+  for (int t = threadIdx.x; t < c.keep - need; t += kSelThreads) stay(need + t, t < last ? older + t : -1);
   if (need == 0) return;
   if (need == older) {
-    for (int t = threadIdx.x; t < need; t += kSelThreads) out[t] = t;
+    for (int t = threadIdx.x; t < need; t += kSelThreads) stay(t, t);
     return;
   }
   const bool held = older <= cap;
   if (held)
-    for (int t = threadIdx.x; t < older; t += kSelThreads) keys[t] = load_key(t);
-  // warp-contiguous pieces, so that the order of the positions is the order of the warps
-  const int per_warp = ((older + 32 * 32 - 1) / (32 * 32)) * 32;
+    for (int t = 4 * threadIdx.x; t < older; t += 4 * kSelThreads) *reinterpret_cast<uint4*>(keys + t) = load_keys(t);
+  // A lane takes four tokens at a time, warps contiguous pieces, so that the order of the positions is the
+  // order of the lanes and warps.
+  const int per_warp = (older + 32 * 128 - 1) / (32 * 128) * 128;
   const int t0 = min(warp * per_warp, older), t1 = min(t0 + per_warp, older);
-  auto key_at = [&](int t) { return held ? keys[t] : load_key(t); };
+  auto keys_at = [&](int t, uint32_t (&k)[4]) {  // 0 behind the piece: below every key but the smallest, and not counted
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (t < t1) x = held ? *reinterpret_cast<const uint4*>(keys + t) : load_keys(t);
+    k[0] = x.x;
+    k[1] = x.y;
+    k[2] = x.z;
+    k[3] = x.w;
+    return min(4, t1 - t);                       // how many of them count
+  };
 
   uint32_t prefix = 0u, mask = 0u;
   int rank = need;  // the rank-th largest among the keys that match the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
     if (threadIdx.x < 256) hist[threadIdx.x] = 0u;
     __syncthreads();
-    for (int base = t0; base < t1; base += 32) {
-      const int t = base + lane;
-      const uint32_t key = t < t1 ? key_at(t) : 0u;
-      const bool in = t < t1 && (key & mask) == prefix;
-      const uint32_t digit = in ? (key >> shift) & 255u : 256u;
-      // equal weights are common (zeros above all): one addition per digit and warp
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+    for (int t = t0 + 4 * lane; t < t1; t += 128) {
+      uint32_t k[4];
+      const int n_k = keys_at(t, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)                // counts: the order does not matter
+        if (e < n_k && (k[e] & mask) == prefix) atomicAdd(&hist[(k[e] >> shift) & 255u], 1u);
     }
     __syncthreads();
     if (warp == 0) {
@@ -230,12 +251,17 @@ cache_select_kernel(Cache c, int cap, const int32_t* __restrict__ lens, const in
   }
   // keys above `prefix` stay, and the first `rank` of those equal to it
   int gt = 0, eq = 0;
-  for (int base = t0; base < t1; base += 32) {
-    const int t = base + lane;
-    const uint32_t key = t < t1 ? key_at(t) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, t < t1 && key > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, t < t1 && key == prefix));
+  for (int t = t0 + 4 * lane; t < t1; t += 128) {
+    uint32_t k[4];
+    const int n_k = keys_at(t, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += e < n_k && k[e] > prefix;
+      eq += e < n_k && k[e] == prefix;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     warp_gt[warp] = gt;
     warp_eq[warp] = eq;
@@ -246,111 +272,109 @@ cache_select_kernel(Cache c, int cap, const int32_t* __restrict__ lens, const in
     gt_before += warp_gt[u];
     eq_before += warp_eq[u];
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int base = t0; base < t1; base += 32) {
-    const int t = base + lane;
-    const uint32_t key = t < t1 ? key_at(t) : 0u;
-    const uint32_t g = __ballot_sync(0xffffffffu, t < t1 && key > prefix);
-    const uint32_t e = __ballot_sync(0xffffffffu, t < t1 && key == prefix);
-    const int my_eq = eq_before + __popc(e & below);
-    if (t < t1 && (key > prefix || (key == prefix && my_eq < rank)))
-      out[gt_before + __popc(g & below) + min(my_eq, rank)] = t;
-    gt_before += __popc(g);
-    eq_before += __popc(e);
+  for (int base = t0; base < t1; base += 128) {
+    const int t = base + 4 * lane;
+    uint32_t k[4];
+    const int n_k = keys_at(t, k);
+    uint32_t mine = 0u;                          // (equal, above) of this lane's four, 16 bits each
+#pragma unroll
+    for (int e = 0; e < 4; ++e) mine += e < n_k ? (k[e] > prefix ? 1u : k[e] == prefix ? 0x10000u : 0u) : 0u;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    int my_gt = gt_before + static_cast<int>((incl - mine) & 0xffffu), my_eq = eq_before + static_cast<int>((incl - mine) >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e >= n_k) continue;
+      if (k[e] > prefix || (k[e] == prefix && my_eq < rank)) stay(my_gt + min(my_eq, rank), t + e);
+      my_gt += k[e] > prefix;
+      my_eq += k[e] == prefix;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+    gt_before += static_cast<int>(all & 0xffffu);
+    eq_before += static_cast<int>(all >> 16);
   }
 }
 
 // ---------------------------------------------------------------------------
 // eviction, second kernel: the kept rows move. One CTA per target block and
-// head: the sources' places and the target's scales in shared memory first,
-// then K and V rows in 16-byte chunks.
+// head. A thread's rows are on their way while the target's scales are found.
 // ---------------------------------------------------------------------------
 
-constexpr int kMoveThreads = 256;
+constexpr int kChunks = 4;  // 16-byte chunks of K and V a thread moves
 
 template <int D>
-__global__ void __launch_bounds__(kMoveThreads)
-cache_move_kernel(Cache c, const int32_t* __restrict__ lens, const int32_t* __restrict__ table, uint8_t* k_codes,
-                  uint8_t* v_codes, float* k_scale, float* v_scale, float* w, const int32_t* __restrict__ dst_table,
-                  const int32_t* __restrict__ kept, unsigned* status) {
+__global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uint8_t* k_codes, uint8_t* v_codes,
+                                  float* k_scale, float* v_scale, float* w, const int32_t* __restrict__ dst_table,
+                                  const int32_t* __restrict__ rows, unsigned* status) {
   constexpr int CH = D / 16;  // chunks of a row
-  __shared__ int src_row[128];            // row of the pool, -1: none
-  __shared__ float ratio[2][128];
-  __shared__ float warp_top[2][4];
+  __shared__ float scale[2][128];
   const int b = blockIdx.y, h = blockIdx.x % c.H_kv, i = blockIdx.x / c.H_kv;
+  const int shift = 31 - __clz(c.block), t = threadIdx.x;
+  pdl_wait();
   const int len = min(max(__ldg(lens + b), 0), c.max_blocks * c.block);
-  const int n = min(len, c.keep);
-  const int first = i * c.block, count = min(c.block, n - first);
-  if (count <= 0) return;
   const int dst = __ldg(dst_table + static_cast<size_t>(b) * c.dst_blocks + i);
+  const int first = i * c.block, count = min(c.block, min(len, c.keep) - first);
+  if (count <= 0) return;
   if (dst < 0 || dst >= c.n_blocks) {
-    if (threadIdx.x == 0) report_status(status, kStatusBadIndex);
+    if (t == 0) report_status(status, kStatusBadIndex);
     return;
   }
-  const size_t dst_head = static_cast<size_t>(dst) * c.H_kv + h;
+  const int32_t* src = rows + (static_cast<size_t>(b) * c.H_kv + h) * c.keep + first;
+  const int dst_head = dst * c.H_kv + h;
+  // chunk e of the block's K rows, then of its V rows; threads: a quarter of both
+  uint4 x[kChunks];
+  int row[kChunks];
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u) {
+    const int e = t + (u % 2) * blockDim.x, r = e / CH;
+    row[u] = r < count ? src[r] : -1;
+  }
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u)
+    if (row[u] >= 0)
+      x[u] = *(reinterpret_cast<const uint4*>((u < 2 ? k_codes : v_codes) + static_cast<size_t>(row[u]) * D) +
+               (t + (u % 2) * blockDim.x) % CH);
   float ks = 0.f, vs = 0.f;
-  const int t = threadIdx.x;
-  if (t < 128) {
-    int row = -1;
-    if (t < count) {
-      const int pos = __ldg(kept + (static_cast<size_t>(b) * c.H_kv + h) * c.keep + first + t);
-      const int blk = __ldg(table + static_cast<size_t>(b) * c.max_blocks + pos / c.block);
-      if (blk >= 0 && blk < c.n_blocks) {
-        const size_t head = static_cast<size_t>(blk) * c.H_kv + h;
-        row = static_cast<int>(head) * c.block + pos % c.block;
-        ks = k_scale[head];
-        vs = v_scale[head];
-        w[dst_head * c.block + t] = w[row];
-      }
+  for (int r = t; r < c.block; r += blockDim.x) {  // blocks of 64-channel rows: two rows a thread
+    const int from = r < count ? src[r] : -1;
+    float a = 0.f, bb = 0.f;
+    if (from >= 0) {
+      a = k_scale[from >> shift];
+      bb = v_scale[from >> shift];
+      w[static_cast<size_t>(dst_head) * c.block + r] = w[from];
     }
-    src_row[t] = row;
-    float kt = ks, vt = vs;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      kt = fmaxf(kt, __shfl_xor_sync(0xffffffffu, kt, o));
-      vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, o));
-    }
-    if (t % 32 == 0) {
-      warp_top[0][t / 32] = kt;
-      warp_top[1][t / 32] = vt;
-    }
+    scale[0][r] = a;
+    scale[1][r] = bb;
   }
   __syncthreads();
-  if (t < 128) {
-    const float kt = fmaxf(fmaxf(warp_top[0][0], warp_top[0][1]), fmaxf(warp_top[0][2], warp_top[0][3]));
-    const float vt = fmaxf(fmaxf(warp_top[1][0], warp_top[1][1]), fmaxf(warp_top[1][2], warp_top[1][3]));
-    ratio[0][t] = kt > 0.f ? ks / kt : 1.f;
-    ratio[1][t] = vt > 0.f ? vs / vt : 1.f;
-    if (t == 0) {
-      k_scale[dst_head] = kt;
-      v_scale[dst_head] = vt;
-    }
+  for (int r = t % 32; r < c.block; r += 32) {
+    ks = fmaxf(ks, scale[0][r]);
+    vs = fmaxf(vs, scale[1][r]);
   }
-  __syncthreads();
-  constexpr int U = 4;  // chunks in flight per thread
-  const int total = 2 * count * CH;
-  for (int e0 = t; e0 < total; e0 += U * kMoveThreads) {
-    uint4 x[U];
-    int row[U], kv[U], ch[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int e = e0 + u * kMoveThreads;
-      kv[u] = e >= count * CH;
-      const int rest = e - kv[u] * count * CH;
-      row[u] = rest / CH;
-      ch[u] = rest % CH;
-      if (e >= total || src_row[row[u]] < 0) row[u] = -1;
-      if (row[u] >= 0) x[u] = *(reinterpret_cast<const uint4*>((kv[u] ? v_codes : k_codes) + static_cast<size_t>(src_row[row[u]]) * D) + ch[u]);
-    }
+  for (int o = 16; o > 0; o >>= 1) {
+    ks = fmaxf(ks, __shfl_xor_sync(0xffffffffu, ks, o));
+    vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, o));
+  }
+  if (t == 0) {
+    k_scale[dst_head] = ks;
+    v_scale[dst_head] = vs;
+  }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (row[u] < 0) continue;
-      const float f = ratio[kv[u]][row[u]];
-      uint4 y = x[u];
-      if (f != 1.f)
-        y = make_uint4(e4m3x4_rescale(y.x, f), e4m3x4_rescale(y.y, f), e4m3x4_rescale(y.z, f), e4m3x4_rescale(y.w, f));
-      *(reinterpret_cast<uint4*>((kv[u] ? v_codes : k_codes) + (dst_head * c.block + row[u]) * D) + ch[u]) = y;
+  for (int u = 0; u < kChunks; ++u) {
+    if (row[u] < 0) continue;
+    const int e = t + (u % 2) * blockDim.x, r = e / CH;
+    const float top = u < 2 ? ks : vs, own = scale[u < 2 ? 0 : 1][r];
+    uint4 y = x[u];
+    if (own != top && top > 0.f) {
+      const Rescale again(own / top);
+      y = make_uint4(again(y.x), again(y.y), again(y.z), again(y.w));
     }
+    *(reinterpret_cast<uint4*>((u < 2 ? k_codes : v_codes) + (static_cast<size_t>(dst_head) * c.block + r) * D) + e % CH) = y;
   }
 }
 
@@ -363,30 +387,23 @@ cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_
   const int touched = (most + c.block - 2) / c.block + 1;  // blocks that `most` tokens can lie in
   const dim3 grid(static_cast<unsigned>(touched) * c.H_kv * 2, c.B);
   const int threads = c.block * c.d / 8 / kPasses;
-  if (c.d == 128)
-    cache_append_kernel<128><<<grid, threads, 0, stream>>>(c, touched, k, v, seq, lens, table, k_codes, v_codes,
-                                                           k_scale, v_scale, w, status);
-  else
-    cache_append_kernel<64><<<grid, threads, 0, stream>>>(c, touched, k, v, seq, lens, table, k_codes, v_codes,
-                                                          k_scale, v_scale, w, status);
-  return cudaGetLastError();
+  return launch_after(c.d == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, grid, dim3(threads), 0, stream, c,
+                      touched, k, v, seq, lens, table, k_codes, v_codes, k_scale, v_scale, w, status);
 }
 
 cudaError_t launch_cache_evict(const Cache& c, const int32_t* lens, const int32_t* table, uint8_t* k_codes,
                                uint8_t* v_codes, float* k_scale, float* v_scale, float* w, const int32_t* dst_table,
-                               int32_t* kept, int32_t* dst_lens, unsigned* status, cudaStream_t stream) {
+                               int32_t* kept, int32_t* dst_lens, int32_t* rows, unsigned* status, cudaStream_t stream) {
   const int cap = min(c.max_blocks * c.block, kSelKeys);
   cudaError_t e = cudaFuncSetAttribute(cache_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
   if (e != cudaSuccess) return e;
-  cache_select_kernel<<<c.B * c.H_kv, kSelThreads, cap * 4, stream>>>(c, cap, lens, table, w, kept, dst_lens, status);
+  e = launch_after(cache_select_kernel, dim3(c.B * c.H_kv), dim3(kSelThreads), cap * 4, stream, c, cap, lens, table, w,
+                   kept, rows, dst_lens, status);
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(c.dst_blocks) * c.H_kv, c.B);
-  if (c.d == 128)
-    cache_move_kernel<128><<<grid, kMoveThreads, 0, stream>>>(c, lens, table, k_codes, v_codes, k_scale, v_scale, w,
-                                                              dst_table, kept, status);
-  else
-    cache_move_kernel<64><<<grid, kMoveThreads, 0, stream>>>(c, lens, table, k_codes, v_codes, k_scale, v_scale, w,
-                                                             dst_table, kept, status);
-  return cudaGetLastError();
+  const int threads = c.block * c.d / 16 * 2 / kChunks;
+  return launch_after(c.d == 128 ? cache_move_kernel<128> : cache_move_kernel<64>, grid, dim3(threads), 0, stream, c, lens,
+                      k_codes, v_codes, k_scale, v_scale, w, dst_table, rows, status);
 }
 
 }  // namespace sda

@@ -58,8 +58,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 32;       // tokens of a tile
-constexpr int kStages = 2;     // tiles in flight per warp
-constexpr int kCtasPerSm = 3;
+constexpr int kStages = 3;     // tiles in flight per warp
+constexpr int kCtasPerSm = 2;
 constexpr int kSms = 148;
 constexpr int kLeast = 8;      // places of a stretch, at least
 // What a unit costs before its first tile (block numbers, scales, Q, the merge at its end: each a chain of

@@ -28,12 +28,37 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
   return f;
 }
 
-// Four codes under a scale, written anew under another: ratio = old / new.
-__device__ __forceinline__ uint32_t e4m3x4_rescale(uint32_t codes, float ratio) {
-  const float2 a = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(codes)));
-  const float2 b = f16x2_to_f32(e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16)));
-  return f32x2_to_e4m3x2(a.x * ratio, a.y * ratio) | f32x2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
 }
+
+// Four codes under a scale, written anew under another: ratio = old / new <= 1.
+// By a power of two fp16 takes the products exactly where they decide: a code
+// has 4 significant bits, so what is not below 2^-10 (which rounds to zero) has
+// its last bit at 2^-13 or above. Other ratios go through fp32.
+struct Rescale {
+  float ratio;
+  uint32_t half2;  // the ratio as fp16, twice, where it is a power of two
+  bool pow2;
+  __device__ __forceinline__ explicit Rescale(float r) {
+    ratio = r;
+    pow2 = (__float_as_uint(r) & 0x7fffffu) == 0u;
+    asm("cvt.rn.f16x2.f32 %0, %1, %1;" : "=r"(half2) : "f"(r));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t codes) const {
+    const uint32_t lo = e4m3x2_to_f16x2(static_cast<uint16_t>(codes)), hi = e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16));
+    if (pow2) {
+      uint32_t a, b;
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(a) : "r"(lo), "r"(half2));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(b) : "r"(hi), "r"(half2));
+      return f16x2_to_e4m3x2(a) | f16x2_to_e4m3x2(b) << 16;
+    }
+    const float2 a = f16x2_to_f32(lo), b = f16x2_to_f32(hi);
+    return f32x2_to_e4m3x2(a.x * ratio, a.y * ratio) | f32x2_to_e4m3x2(b.x * ratio, b.y * ratio) << 16;
+  }
+};
 
 // Sequence b's new rows and tokens, clamped to what the tensors hold.
 struct NewRows {

@@ -53,13 +53,13 @@ struct CacheLayout {
 };
 CacheLayout make_cache_layout(const Cache& c);
 
-// cache.cu
+// cache.cu. Eviction keeps each target's source row in `rows` ([B, H_kv, keep], in the workspace behind the status).
 cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_t* v, const int32_t* seq,
                                 const int32_t* lens, const int32_t* table, uint8_t* k_codes, uint8_t* v_codes,
                                 float* k_scale, float* v_scale, float* w, unsigned* status, cudaStream_t stream);
 cudaError_t launch_cache_evict(const Cache& c, const int32_t* lens, const int32_t* table, uint8_t* k_codes,
                                uint8_t* v_codes, float* k_scale, float* v_scale, float* w, const int32_t* dst_table,
-                               int32_t* kept, int32_t* dst_lens, unsigned* status, cudaStream_t stream);
+                               int32_t* kept, int32_t* dst_lens, int32_t* rows, unsigned* status, cudaStream_t stream);
 
 // cache_attn.cu
 cudaError_t launch_cache_attn(const Cache& c, const CacheLayout& y, void* ws, const uint16_t* q, const int32_t* seq,

@@ -153,6 +153,9 @@ int32_t check_pool(const int32_t* lens, const int32_t* table, const uint8_t* k_c
   return check_ptr(v_scale, "v_scale");
 }
 
+// Eviction's scratch behind the status word: the row of the pool that each target comes from.
+size_t evict_rows_bytes(const Cache& C) { return static_cast<size_t>(C.B) * C.H_kv * C.keep * 4; }
+
 int32_t need_rows(const Cache& C) {
   if (C.rows < 1 || C.max_new < 1) return fail(SDA_ERR_SHAPE, "rows and max_new must be >= 1 for this call");
   return SDA_OK;
@@ -190,7 +193,8 @@ int32_t sda_prompt_attn_fwd(const sda_prompt_params* p, const uint16_t* q, const
 size_t sda_cache_workspace_size(const sda_cache_params* p) {
   Cache C;
   if (make_cache(p, &C) != SDA_OK) return 0;
-  return sda::make_cache_layout(C).total;
+  const size_t attn = C.max_new > 0 ? sda::make_cache_layout(C).total : 256, evict = 256 + evict_rows_bytes(C);
+  return attn > evict ? attn : evict;
 }
 
 int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uint16_t* v, const int32_t* seq,
@@ -246,7 +250,7 @@ int32_t sda_cache_evict(const sda_cache_params* p, const int32_t* lens, const in
   Cache C;
   SDA_TRY(make_cache(p, &C));
   if (C.keep < 1) return fail(SDA_ERR_SHAPE, "keep must be >= 1 for this call");
-  SDA_TRY(check_ws(256, ws, ws_bytes));
+  SDA_TRY(check_ws(256 + evict_rows_bytes(C), ws, ws_bytes));
   SDA_TRY(check_pool(lens, block_table, k_codes, v_codes, k_scale, v_scale));
   SDA_TRY(check_ptr(w, "w"));
   SDA_TRY(check_ptr(dst_table, "dst_table"));
@@ -254,7 +258,7 @@ int32_t sda_cache_evict(const sda_cache_params* p, const int32_t* lens, const in
   SDA_TRY(check_ptr(dst_lens, "dst_lens"));
   SDA_TRY(sda::require_device());
   return launched(sda::launch_cache_evict(C, lens, block_table, k_codes, v_codes, k_scale, v_scale, w, dst_table, kept,
-                                          dst_lens, at<unsigned>(ws, 0), static_cast<cudaStream_t>(stream)),
+                                          dst_lens, at<int32_t>(ws, 256), at<unsigned>(ws, 0), static_cast<cudaStream_t>(stream)),
                   "cache eviction");
 }
 
