@@ -13,15 +13,18 @@
 // same key head (equal work under the causal mask) or, where the heads of a
 // key head are odd in number, two adjacent row tiles of one head.
 //
-// Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 issues every
-// MMA, 2 finds the CTA's tile and owns TMEM, 3 clears V rows behind the
-// sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1, a thread per row.
+// Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 and 2 issue
+// the MMAs of tile 0 and 1 (2 also finds the CTA's tile and owns TMEM), 3 clears V
+// rows behind the sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1,
+// a thread per row. An issuing thread blocks while the tensor pipe is busy, so
+// one for both tiles left the pipe idle through its waits (a pair of steps took
+// 4,020 cycles with one, MEASURE with two).
 //
-// The MMAs of one thread execute in order, so the issue order
-//   PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)
-// lets P_w overlay S_w in TMEM (bf16, half the columns): QK_w(j+1) comes
-// after PV_w(j) has read P_w, and S_w(j+1) ready implies PV_w(j) done, so the
-// softmax may rescale O_w without another wait. It does so only when a row's
+// The MMAs of one thread execute in order, so the issue order PV_w(j),
+// QK_w(j+1) lets P_w overlay S_w in TMEM (bf16, half the columns): QK_w(j+1)
+// comes after PV_w(j) has read P_w, and S_w(j+1) ready implies PV_w(j) done, so
+// the softmax may rescale O_w without another wait. P_w is handed over in two
+// halves: the product of the first runs under the exponentials of the second. It does so only when a row's
 // maximum grows by more than 2^8 (exact: numerator and denominator share the
 // reference). P is rounded to bf16 (the type of V, as the MMA asks); the sum
 // takes the unrounded fp32 values.
@@ -68,7 +71,10 @@ struct Smem {
   static constexpr int kTotal = kBars + 512;
 };
 
-enum { B_QFULL = 0, B_SFULL = 2, B_PFULL = 4, B_ODONE = 6, B_VLAST = 8, B_VCLEAR = 9, B_DRAIN = 10, B_FULL = 11 };  // + ring full, ring empty
+enum {  // w: tile
+  B_QFULL = 0, B_SFULL = 2, B_PHALF = 4, B_PFULL = 6, B_ODONE = 8, B_DRAIN = 10, B_VLAST = 12, B_VCLEAR = 13,
+  B_FULL = 14  // ring full, then ring empty
+};
 
 // What the CTA works on, found by one warp.
 struct Item {
@@ -162,6 +168,33 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   }
 }
 
+// tcgen05.mma and commit for a whole warp: the lane with `leader` != 0 issues.
+__device__ __forceinline__ void mma_ss_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader)
+      : "memory");
+}
+
 __device__ __forceinline__ uint32_t sw(uint32_t row, uint32_t chunk) { return tc::sw128_offset(row, chunk); }
 
 template <int D>
@@ -184,7 +217,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   int* bad_flag = reinterpret_cast<int*>(tail + 8);
   Item* item = reinterpret_cast<Item*>(tail + 16);
 
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // through a shuffle, so that the compiler knows it to be the same for the warp
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int groups = pair_heads ? p.H / 2 : p.H;  // head groups, fastest: they share the tile's K and V through L2
   const int hg = blockIdx.x % groups;
   const int R = pair_heads ? kTile : 2 * kTile;
@@ -193,12 +227,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&bars[B_QFULL + w], 1);
       tc::mbar_init(&bars[B_SFULL + w], 1);
-      tc::mbar_init(&bars[B_PFULL + w], 128);
+      tc::mbar_init(&bars[B_PFULL + w], 4);  // a warp each
       tc::mbar_init(&bars[B_ODONE + w], 1);
+      tc::mbar_init(&bars[B_DRAIN + w], 1);
     }
     tc::mbar_init(&bars[B_VLAST], 1);
     tc::mbar_init(&bars[B_VCLEAR], 32);
-    tc::mbar_init(&bars[B_DRAIN], 1);
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -223,7 +257,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   const Span seq{item->q0, item->nq, item->k0, item->nk};
   const int row0 = item->t * R;
@@ -235,7 +269,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   const bool live_1 = row_1 < seq.nq;
   const int n0 = (keys_below(p, seq, end_0) + kTile - 1) / kTile;
   const int n1 = live_1 ? (keys_below(p, seq, end_1) + kTile - 1) / kTile : 0;
-  const int n = max(n0, n1);
+  const int n = __shfl_sync(0xffffffffu, max(n0, n1), 0);
 
   if (warp < 4) {
     tc::setmaxnreg_dec<kRegsLow>();
@@ -268,66 +302,77 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if ((w ? n1 : n0) > 0) tc::wait1(&bars[B_QFULL + w], 0, &never);
       for (int b = c > NS ? c - NS : 0; b < c; ++b)
         tc::wait1(b == 2 * n - 1 ? &bars[B_VLAST] : &full[b % NS], b == 2 * n - 1 ? 0 : (b / NS) & 1, &never);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
+      // The whole warp walks the loop, so that descriptors and addresses are uniform values; one lane issues. With
+      // one lane in a branch of its own they were moved between register files for every MMA, and the pipe waited
+      // for them (a pair of steps took 3,880 cycles, MEASURE like this).
       constexpr uint32_t idesc_qk = tc::idesc_bf16(128, 128, false);
       constexpr uint32_t idesc_pv = tc::idesc_bf16(128, D, true);  // B = V, MN-major
+      const uint32_t leader = lane == 0;
+      const int m0 = __shfl_sync(0xffffffffu, n0, 0), m1 = __shfl_sync(0xffffffffu, n1, 0);
+      const uint64_t desc_k0 = tc::smem_desc_sw128(smem + S::kRing, 16, 1024);           // K: K-major
+      const uint64_t desc_v0 = tc::smem_desc_sw128(smem + S::kRing, kTile * 128, 1024);  // V: MN-major
+      const uint64_t desc_q0 = tc::smem_desc_sw128(smem + S::kQ, 16, 1024);
+      constexpr uint32_t kTile16 = S::kTileBytes / 16, kHalf16 = kTile * 128 / 16;       // descriptors count in 16 bytes
       bool ok = true;
-      auto stage_of = [&](int c) { return smem + S::kRing + (c % NS) * S::kTileBytes; };
-      auto wait_full = [&](int c) { return tc::wait1(&full[c % NS], (c / NS) & 1, abort_flag, wait_ns); };
-      auto qk = [&](int w, int j) {
-        const unsigned char* kst = stage_of(2 * j);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::wait_warp(bar, parity, abort_flag, wait_ns); };
+      auto qk = [&](int w, int st) {
+        const uint64_t da = desc_q0 + w * kTile16, db = desc_k0 + st * kTile16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const int hf = kk / 4, c = kk % 4;
-          const uint64_t da =
-              tc::smem_desc_sw128(smem + S::kQ + w * S::kTileBytes + hf * kTile * 128 + c * 32, 16, 1024);
-          const uint64_t db = tc::smem_desc_sw128(kst + hf * kTile * 128 + c * 32, 16, 1024);
-          tc::mma_ss(tmem + kColS + 128 * w, da, db, idesc_qk, kk > 0 ? 1u : 0u);
+          const uint32_t at = kk / 4 * kHalf16 + kk % 4 * 2;
+          mma_ss_by(leader, tmem + kColS + 128 * w, da + at, db + at, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        tc::commit(&bars[B_SFULL + w]);
+        commit_by(leader, &bars[B_SFULL + w]);
       };
-      if (n > 0) ok = wait_full(0);
-      for (int w = 0; w < 2 && ok; ++w) {
-        if ((w ? n1 : n0) == 0) continue;
-        ok = tc::wait1(&bars[B_QFULL + w], 0, abort_flag, wait_ns);
-        if (!ok) break;
+      auto pv = [&](int w, int st, uint32_t acc) {
+        const uint64_t db = desc_v0 + st * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts_by(leader, tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db + kk * 128, idesc_pv,
+                    kk > 0 ? 1u : acc);
+      };
+      if (n > 0) ok = wait(&full[0], 0);
+      if (ok && m0 > 0) {
+        ok = wait(&bars[B_QFULL], 0);
         tc::fence_after_sync();
-        qk(w, 0);
+        if (ok) qk(0, 0);
       }
-      if (ok && n > 0) tc::commit(&empty[0]);
+      if (ok && m1 > 0) {
+        ok = wait(&bars[B_QFULL + 1], 0);
+        tc::fence_after_sync();
+        if (ok) qk(1, 0);
+      }
+      if (ok && n > 0) commit_by(leader, &empty[0]);
+      int sv = 1, v_par = 0, sk = 2, k_par = 0;  // stages and parities of V_j and K_{j+1}
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
-        const int cv = 2 * j + 1, ck = 2 * j + 2;
-        const unsigned char* vst = stage_of(cv);
-        ok = j == n - 1 ? tc::wait1(&bars[B_VCLEAR], 0, abort_flag, wait_ns) : wait_full(cv);
-        bool have_k = false;
-        for (int w = 0; w < 2 && ok; ++w) {
-          const int nw = w ? n1 : n0;
+        ok = j == n - 1 ? wait(&bars[B_VCLEAR], 0) : wait(&full[sv], v_par);
+        if (ok && j + 1 < n) ok = wait(&full[sk], k_par);
+        if (!ok) break;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const int nw = w ? m1 : m0;
           if (j >= nw) continue;
-          ok = tc::wait1(&bars[B_PFULL + w], j & 1, abort_flag, wait_ns);
+          ok = wait(&bars[B_PFULL + w], j & 1);
           if (!ok) break;
           tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
-            const uint64_t db = tc::smem_desc_sw128(vst + kk * 16 * 128, kTile * 128, 1024);
-            tc::mma_ts(tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db, idesc_pv,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-          }
-          if (j == nw - 1) tc::commit(&bars[B_ODONE + w]);
-          if (j + 1 < nw) {
-            if (!have_k) ok = wait_full(ck);
-            if (!ok) break;
-            have_k = true;
-            qk(w, j + 1);
-          }
+          pv(w, sv, j > 0);
+          if (j == nw - 1) commit_by(leader, &bars[B_ODONE + w]);
+          else qk(w, sk);
         }
         if (!ok) break;
-        tc::commit(&empty[cv % NS]);
-        if (j + 1 < n) tc::commit(&empty[ck % NS]);
+        commit_by(leader, &empty[sv]);
+        if (j + 1 < n) commit_by(leader, &empty[sk]);
+        sv += 2;
+        if (sv >= NS) sv -= NS, v_par ^= 1;
+        sk += 2;
+        if (sk >= NS) sk -= NS, k_par ^= 1;
       }
-      // drain: every MMA this thread issued
-      tc::commit(&bars[B_DRAIN]);
-      tc::wait1(&bars[B_DRAIN], 0, &never);
+      // drain: every MMA this warp issued
+      commit_by(leader, &bars[B_DRAIN]);
+      tc::wait_warp(&bars[B_DRAIN], 0, &never);
     } else if (warp == 3 && n > 0) {
       // ------------------------------------------------------------ V rows behind the sequence
       const int c = 2 * n - 1;  // the last V tile
@@ -377,21 +422,50 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = c < vis ? s[c] : -INFINITY;
       }
-      float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
+      auto row_max = [&] {
+        float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
 #pragma unroll
-      for (int c = 8; c < 128; c += 8) {
-        a0 = max3(a0, s[c], s[c + 1]);
-        a1 = max3(a1, s[c + 2], s[c + 3]);
-        a2 = max3(a2, s[c + 4], s[c + 5]);
-        a3 = max3(a3, s[c + 6], s[c + 7]);
-      }
-      const float mx = max3(a0, a1, fmaxf(a2, a3)) * p.scale_log2;
-      if (j == 0) {
-        m = mx;
-      } else {
+        for (int c = 8; c < 128; c += 8) {
+          a0 = max3(a0, s[c], s[c + 1]);
+          a1 = max3(a1, s[c + 2], s[c + 3]);
+          a2 = max3(a2, s[c + 4], s[c + 5]);
+          a3 = max3(a3, s[c + 6], s[c + 7]);
+        }
+        return max3(a0, a1, fmaxf(a2, a3)) * p.scale_log2;
+      };
+      if (j == 0) m = row_max();
+      // The exponentials begin with the reference so far; whether the step's maximum is within 2^8 of it is seen
+      // under their latency, and if it is not (rarely) they are taken again.
+      const uint64_t sc2 = f2(p.scale_log2, p.scale_log2);
+      for (;;) {
+        const float mref = (m == -INFINITY) ? 0.f : m;
+        const uint64_t nm2 = f2(-mref, -mref);
+        uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
+        float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = 16 * ch + e;  // key pair 2c, 2c + 1
+            float x0, x1;
+            f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), sc2, nm2), x0, x1);
+            const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);  // 2^-inf = 0 on hidden keys
+            if (e & 1) {
+              acc1 = add2(acc1, f2(p0, p1));
+              a1 = max3(a1, s[2 * c], s[2 * c + 1]);
+            } else {
+              acc0 = add2(acc0, f2(p0, p1));
+              a0 = max3(a0, s[2 * c], s[2 * c + 1]);
+            }
+            pk[e] = pack_bf16(p0, p1);
+          }
+          tc::tmem_st16p(t_s + 16 * ch, pk);
+        }
+        const float mx = fmaxf(a0, a1) * p.scale_log2;
         const bool grow = mx > m + 8.0f;
         if (__any_sync(0xffffffffu, grow)) {
-          // S_w(j) ready: PV_w(j - 1) is done and O_w rests
+          // S_w(j) ready: PV_w(j - 1) is done and O_w rests (there is none yet at j = 0, and no growth)
           const float alpha = !grow ? 1.f : (m == -INFINITY ? 0.f : tc::ex2(m - mx));
           if (grow) {
             l *= alpha;
@@ -406,35 +480,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
             tc::tmem_st16p(t_o + 16 * c, r);
           }
-          tc::tmem_wait_st();
+          continue;
         }
-      }
-      const float mref = (m == -INFINITY) ? 0.f : m;
-      const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nm2 = f2(-mref, -mref);
-      uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = 16 * ch + e;  // key pair 2c, 2c + 1
-          float x0, x1;
-          f2_split(fma2(f2(s[2 * c], s[2 * c + 1]), sc2, nm2), x0, x1);
-          const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);  // 2^-inf = 0 on hidden keys
-          if (e & 1) acc1 = add2(acc1, f2(p0, p1));
-          else acc0 = add2(acc0, f2(p0, p1));
-          pk[e] = pack_bf16(p0, p1);
-        }
-        tc::tmem_st16p(t_s + 16 * ch, pk);
-      }
-      {
         float r0, r1;
         f2_split(add2(acc0, acc1), r0, r1);
         l += r0 + r1;
+        break;
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&bars[B_PFULL + w]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars[B_PFULL + w]);
     }
     const bool live = w == 0 || live_1;
     if (ok && nw > 0) ok = tc::wait_warp(&bars[B_ODONE + w], 0, abort_flag, wait_ns);
