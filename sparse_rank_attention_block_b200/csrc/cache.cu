@@ -18,9 +18,9 @@ namespace sda {
 namespace {
 
 // ---------------------------------------------------------------------------
-// append: one CTA per touched block, head and K or V; the block's new rows stay
-// in registers between their maximum and their encoding. A thread holds a
-// 16-byte chunk (8 channels) of up to kPasses rows.
+// append: a CTA takes one touched block and some of its units (a head's K or V);
+// a unit's new rows stay in registers between their maximum and their encoding. A
+// thread holds a 16-byte chunk (8 channels) of up to kPasses rows.
 // ---------------------------------------------------------------------------
 
 constexpr int kPasses = 4;
@@ -34,97 +34,106 @@ __device__ __forceinline__ float wanted_scale(uint32_t amax_bf16) {
 }
 
 template <int D>
-__global__ void cache_append_kernel(Cache c, int touched, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
-                                    const int32_t* __restrict__ seq, const int32_t* __restrict__ lens,
-                                    const int32_t* __restrict__ table, uint8_t* __restrict__ k_codes,
-                                    uint8_t* __restrict__ v_codes, float* __restrict__ k_scale,
-                                    float* __restrict__ v_scale, float* __restrict__ w, unsigned* status) {
+__global__ void cache_append_kernel(Cache c, int touched, int units, const uint16_t* __restrict__ k,
+                                    const uint16_t* __restrict__ v, const int32_t* __restrict__ seq,
+                                    const int32_t* __restrict__ lens, const int32_t* __restrict__ table,
+                                    uint8_t* __restrict__ k_codes, uint8_t* __restrict__ v_codes,
+                                    float* __restrict__ k_scale, float* __restrict__ v_scale, float* __restrict__ w,
+                                    unsigned* status) {
   constexpr int CH = D / 8;  // chunks of a row
-  __shared__ uint32_t warp_max[32];
-  const int b = blockIdx.y;
-  const int is_v = blockIdx.x & 1, h = (blockIdx.x >> 1) % c.H_kv, i = (blockIdx.x >> 1) / c.H_kv;
+  __shared__ uint32_t warp_max[2][32];
+  const int b = blockIdx.y, i = blockIdx.x % touched, u0 = blockIdx.x / touched * units;
   bool bad = false;
   pdl_wait();
   const NewRows r = new_rows(c, seq, lens, b, bad);
   bad = bad || r.first < 0;
   const int start = max(r.first, 0);
-  const int bi = start / c.block + i;                         // block of the sequence
+  const int bi = (start >> (31 - __clz(c.block))) + i;        // block of the sequence
   const int lo = max(bi * c.block, start);                    // its new positions [lo, hi)
   const int hi = min(min((bi + 1) * c.block, r.first + r.n), c.max_blocks * c.block);
   if (threadIdx.x == 0 && blockIdx.x == 0 && bad) report_status(status, kStatusBadIndex);
-  if (i >= touched || lo >= hi || bi >= c.max_blocks) return;
+  if (lo >= hi || bi >= c.max_blocks) return;
   const int blk = __ldg(table + static_cast<size_t>(b) * c.max_blocks + bi);
   if (blk < 0 || blk >= c.n_blocks) {
     if (threadIdx.x == 0) report_status(status, kStatusBadIndex);
     return;
   }
-  const uint16_t* src = is_v ? v : k;
-  const long long ld = is_v ? c.ld_v : c.ld_k;
-  const size_t head = static_cast<size_t>(blk) * c.H_kv + h;
-  uint8_t* codes = (is_v ? v_codes : k_codes) + head * c.block * D;
-  float* scale = (is_v ? v_scale : k_scale) + head;
   const int slot0 = lo - bi * c.block, n = hi - lo;           // slots [slot0, slot0 + n); older tokens before them
   const int ch = threadIdx.x % CH, row0 = threadIdx.x / CH, step = blockDim.x / CH;
-  const float before = slot0 > 0 ? *scale : 0.f;
-
-  uint4 x[kPasses];
-  uint32_t m2 = 0u;  // two 16-bit magnitudes
   const size_t first_row = static_cast<size_t>(r.row0) + (lo - r.first);
+  const int u1 = min(u0 + units, 2 * c.H_kv);
+  // unit u: head u / 2, K or V; the next unit's rows are on their way while one is encoded
+  uint4 x[kPasses];
+  auto read = [&](int u) {
+    const uint16_t* src = u & 1 ? v : k;
+    const long long ld = u & 1 ? c.ld_v : c.ld_k;
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int row = row0 + p * step;
-    x[p] = row < n ? __ldcs(reinterpret_cast<const uint4*>(src + (first_row + row) * ld + h * D) + ch)
-                   : make_uint4(0u, 0u, 0u, 0u);
-  }
+    for (int p = 0; p < kPasses; ++p) {
+      const int row = row0 + p * step;
+      x[p] = row < n ? __ldcs(reinterpret_cast<const uint4*>(src + (first_row + row) * ld + (u >> 1) * D) + ch)
+                     : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
   // |x| of a bf16 orders like its bits without the sign; infinities and NaN (>= 0x7f80) do not count
   auto magnitude = [](uint32_t two) {
-    const uint32_t a = two & 0x7fffu, bb = (two >> 16) & 0x7fffu;
-    return (a < 0x7f80u ? a : 0u) | (bb < 0x7f80u ? bb : 0u) << 16;
+    const uint32_t lo16 = two & 0x7fffu, hi16 = (two >> 16) & 0x7fffu;
+    return (lo16 < 0x7f80u ? lo16 : 0u) | (hi16 < 0x7f80u ? hi16 : 0u) << 16;
   };
+  read(u0);
+  for (int u = u0; u < u1; ++u) {
+    const size_t head = static_cast<size_t>(blk) * c.H_kv + (u >> 1);
+    uint8_t* codes = (u & 1 ? v_codes : k_codes) + head * c.block * D;
+    float* scale = (u & 1 ? v_scale : k_scale) + head;
+    const float before = slot0 > 0 ? *scale : 0.f;
+    uint32_t m2 = 0u;  // two 16-bit magnitudes
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    m2 = __vmaxu2(m2, __vmaxu2(magnitude(x[p].x), magnitude(x[p].y)));
-    m2 = __vmaxu2(m2, __vmaxu2(magnitude(x[p].z), magnitude(x[p].w)));
-  }
-  uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
-  const int warps = blockDim.x / 32;
-  if (warps > 1) {
-    if (threadIdx.x % 32 == 0) warp_max[threadIdx.x / 32] = m;
-    __syncthreads();
-    m = warp_max[0];
-    for (int u = 1; u < warps; ++u) m = max(m, warp_max[u]);
-  }
-  const float want = wanted_scale(m);
-  const float after = slot0 > 0 ? fmaxf(before, want) : want;
-  // every thread has read the old scale before it changes (the barrier above; one warp: program order)
-  if (warps == 1) __syncwarp();
-  if (threadIdx.x == 0) *scale = after;
-  if (slot0 > 0) {
-    const Rescale again(before / after);
-    if (before != after)
+    for (int p = 0; p < kPasses; ++p) {
+      m2 = __vmaxu2(m2, __vmaxu2(magnitude(x[p].x), magnitude(x[p].y)));
+      m2 = __vmaxu2(m2, __vmaxu2(magnitude(x[p].z), magnitude(x[p].w)));
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+    const int warps = blockDim.x / 32;
+    uint32_t* tops = warp_max[u & 1];  // two in turn: one barrier a unit is enough
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = m;
+    __syncthreads();                   // every thread has read the old scale, too
+    for (int g = 0; g < warps; ++g) m = max(m, tops[g]);
+    const float want = wanted_scale(m);
+    const float after = slot0 > 0 ? fmaxf(before, want) : want;
+    if (threadIdx.x == 0) *scale = after;
+    if (slot0 > 0 && before != after) {
+      const Rescale again(before / after);
       for (int row = row0; row < slot0; row += step) {
         uint2* at = reinterpret_cast<uint2*>(codes + row * D) + ch;
         const uint2 old = *at;
         *at = make_uint2(again(old.x), again(old.y));
       }
-  }
-  // x / scale: for a power of two (every scale that append chose) the product with its inverse is the quotient
-  const bool pow2 = (__float_as_uint(after) & 0x7fffffu) == 0u;
-  const float inv = 1.f / after;
-  auto scaled = [&](float f) { return pow2 ? f * inv : f / after; };
+    }
+    // x / scale: for a power of two (every scale that append chose) the product with its inverse is the quotient
+    const bool pow2 = (__float_as_uint(after) & 0x7fffffu) == 0u;
+    const float inv = 1.f / after;
+    uint2 out[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    const int row = row0 + p * step;
-    if (row < n) {
+    for (int p = 0; p < kPasses; ++p) {
       const uint32_t in[4] = {x[p].x, x[p].y, x[p].z, x[p].w};
       uint32_t two[4];
+      if (pow2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) two[e] = f32x2_to_e4m3x2(scaled(bf16_lo(in[e])), scaled(bf16_hi(in[e])));
-      *(reinterpret_cast<uint2*>(codes + (slot0 + row) * D) + ch) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+        for (int e = 0; e < 4; ++e) two[e] = f32x2_to_e4m3x2(bf16_lo(in[e]) * inv, bf16_hi(in[e]) * inv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) two[e] = f32x2_to_e4m3x2(bf16_lo(in[e]) / after, bf16_hi(in[e]) / after);
+      }
+      out[p] = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
     }
+    if (u + 1 < u1) read(u + 1);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const int row = row0 + p * step;
+      if (row < n) *(reinterpret_cast<uint2*>(codes + (slot0 + row) * D) + ch) = out[p];
+    }
+    if (w != nullptr && !(u & 1))
+      for (int row = threadIdx.x; row < n; row += blockDim.x) w[head * c.block + slot0 + row] = 0.f;
   }
-  if (w != nullptr && !is_v)
-    for (int row = threadIdx.x; row < n; row += blockDim.x) w[head * c.block + slot0 + row] = 0.f;
 }
 
 // ---------------------------------------------------------------------------
@@ -312,6 +321,7 @@ __global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uin
                                   const int32_t* __restrict__ rows, unsigned* status) {
   constexpr int CH = D / 16;  // chunks of a row
   __shared__ float scale[2][128];
+  __shared__ float ratio[2][128];
   const int b = blockIdx.y, h = blockIdx.x % c.H_kv, i = blockIdx.x / c.H_kv;
   const int shift = 31 - __clz(c.block), t = threadIdx.x;
   pdl_wait();
@@ -338,7 +348,6 @@ __global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uin
     if (row[u] >= 0)
       x[u] = *(reinterpret_cast<const uint4*>((u < 2 ? k_codes : v_codes) + static_cast<size_t>(row[u]) * D) +
                (t + (u % 2) * blockDim.x) % CH);
-  float ks = 0.f, vs = 0.f;
   for (int r = t; r < c.block; r += blockDim.x) {  // blocks of 64-channel rows: two rows a thread
     const int from = r < count ? src[r] : -1;
     float a = 0.f, bb = 0.f;
@@ -351,27 +360,31 @@ __global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uin
     scale[1][r] = bb;
   }
   __syncthreads();
+  // scales are positive: their bits order like their values
+  uint32_t k_top = 0u, v_top = 0u;
   for (int r = t % 32; r < c.block; r += 32) {
-    ks = fmaxf(ks, scale[0][r]);
-    vs = fmaxf(vs, scale[1][r]);
+    k_top = max(k_top, __float_as_uint(scale[0][r]));
+    v_top = max(v_top, __float_as_uint(scale[1][r]));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ks = fmaxf(ks, __shfl_xor_sync(0xffffffffu, ks, o));
-    vs = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, o));
-  }
+  const float ks = __uint_as_float(__reduce_max_sync(0xffffffffu, k_top));
+  const float vs = __uint_as_float(__reduce_max_sync(0xffffffffu, v_top));
   if (t == 0) {
     k_scale[dst_head] = ks;
     v_scale[dst_head] = vs;
   }
+  for (int r = t; r < c.block; r += blockDim.x) {
+    ratio[0][r] = ks > 0.f ? scale[0][r] / ks : 1.f;
+    ratio[1][r] = vs > 0.f ? scale[1][r] / vs : 1.f;
+  }
+  __syncthreads();
 #pragma unroll
   for (int u = 0; u < kChunks; ++u) {
     if (row[u] < 0) continue;
     const int e = t + (u % 2) * blockDim.x, r = e / CH;
-    const float top = u < 2 ? ks : vs, own = scale[u < 2 ? 0 : 1][r];
+    const float f = ratio[u < 2 ? 0 : 1][r];
     uint4 y = x[u];
-    if (own != top && top > 0.f) {
-      const Rescale again(own / top);
+    if (f != 1.f) {
+      const Rescale again(f);
       y = make_uint4(again(y.x), again(y.y), again(y.z), again(y.w));
     }
     *(reinterpret_cast<uint4*>((u < 2 ? k_codes : v_codes) + (static_cast<size_t>(dst_head) * c.block + r) * D) + e % CH) = y;
@@ -385,10 +398,13 @@ cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_
                                 float* k_scale, float* v_scale, float* w, unsigned* status, cudaStream_t stream) {
   const int most = min(c.max_new, c.rows);
   const int touched = (most + c.block - 2) / c.block + 1;  // blocks that `most` tokens can lie in
-  const dim3 grid(static_cast<unsigned>(touched) * c.H_kv * 2, c.B);
+  // Single tokens: a CTA per unit, for latency. Prompts: four units a CTA, since most CTAs of a batch of unequal
+  // prompts find nothing to do (6 prompts of 300 to 9,001 tokens: 26 us with one unit, MEASURE with four).
+  const int units = touched > 1 ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>(touched) * ((2 * c.H_kv + units - 1) / units), c.B);
   const int threads = c.block * c.d / 8 / kPasses;
   return launch_after(c.d == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, grid, dim3(threads), 0, stream, c,
-                      touched, k, v, seq, lens, table, k_codes, v_codes, k_scale, v_scale, w, status);
+                      touched, units, k, v, seq, lens, table, k_codes, v_codes, k_scale, v_scale, w, status);
 }
 
 cudaError_t launch_cache_evict(const Cache& c, const int32_t* lens, const int32_t* table, uint8_t* k_codes,
