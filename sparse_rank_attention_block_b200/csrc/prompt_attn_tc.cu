@@ -46,6 +46,7 @@
 
 #include "common.cuh"
 #include "ex2_fma.cuh"
+#include "launch.cuh"
 #include "serving.h"
 #include "tc.cuh"
 
@@ -134,6 +135,11 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
   top = __reduce_max_sync(0xffffffffu, top);
   out->valid = 0;
+  if (p.n_seq == 1) {  // one sequence: its tiles from the last
+    const int T = (mine.nq + R - 1) / R;
+    if (lane == 0 && i < T) *out = Item{1, mine.q0, mine.nq, mine.k0, mine.nk, T - 1 - i};
+    return;
+  }
   if (i >= over(-1)) return;
   int lo = 0, hi = (top + kTile - 1) / kTile;  // over(hi) = 0 <= i
   while (lo < hi) {
@@ -214,7 +220,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   unsigned char* tail = smem + S::kBars + 8 * (B_FULL + 2 * NS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
-  int* bad_flag = reinterpret_cast<int*>(tail + 8);
   Item* item = reinterpret_cast<Item*>(tail + 16);
 
   // through a shuffle, so that the compiler knows it to be the same for the warp
@@ -237,27 +242,29 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
     }
-    *abort_flag = (*reinterpret_cast<volatile unsigned*>(status) & kStatusTimeout) ? 1 : 0;
-    *bad_flag = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch(&tm_q);
     tc::tma_prefetch(&tm_k);
     tc::tma_prefetch(&tm_v);
   }
+  if (warp == 3) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::fence_before_sync();
+  }
+  pdl_wait();
+  if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile unsigned*>(status) & kStatusTimeout) ? 1 : 0;
   if (warp == 2) {
     bool bad = false;
     find_item(p, seq_q, seq_k, R, blockIdx.x / groups, item, bad);
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report_status(status, kStatusBadIndex);
   }
   __syncthreads();
-  if (*abort_flag || !item->valid) return;  // uniform
-  if (warp == 2) {
-    tc::tmem_alloc(tmem_slot, kTmemCols);
-    tc::fence_before_sync();
-  }
-  __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  if (*abort_flag || !item->valid) {  // uniform
+    if (warp == 3) tc::tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   const Span seq{item->q0, item->nq, item->k0, item->nk};
   const int row0 = item->t * R;
@@ -543,7 +550,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   tc::fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) report_status(status, kStatusTimeout);
-  if (warp == 2) {
+  if (warp == 3) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
@@ -605,9 +612,8 @@ cudaError_t run(const Prompt& p, const uint16_t* q, const uint16_t* k, const uin
   const int R = pair_heads ? kTile : 2 * kTile;
   const long long tiles = static_cast<long long>(p.rows_q) / R + p.n_seq;  // at least the sequences' row tiles
   const long long blocks = tiles * (pair_heads ? p.H / 2 : p.H);
-  prompt_attn_kernel<D><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(
-      mq, mk, mv, p, pair_heads, seq_q, seq_k, o, lse, status, attention_wait_limit());
-  return cudaGetLastError();
+  return launch_after(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, mq, mk, mv, p,
+                      pair_heads, seq_q, seq_k, o, lse, status, attention_wait_limit());
 }
 
 }  // namespace
