@@ -404,7 +404,8 @@ int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uin
  * w_out (or NULL; needs weights = 1): w_out[slot] = w_in[slot] + the sum of the token's p over the
  * call's rows and the key head's query heads, for every token of the B
  * sequences; other slots of w_out stay as they are. w_in NULL counts as zeros;
- * w_in may be w_out. Rows over max_new, tokens in blocks outside the pool and
+ * w_in may be w_out. Sequences may share blocks when w_out is NULL; with it a
+ * block belongs to one sequence. Rows over max_new, tokens in blocks outside the pool and
  * tokens past max_blocks * block are left out and reported. NaN or infinity in a
  * cached token reaches the rows of its sequence. */
 int32_t sda_cache_attn_fwd(const sda_cache_params* p, const uint16_t* q, const int32_t* seq, const int32_t* lens,

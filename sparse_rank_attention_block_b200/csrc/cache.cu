@@ -7,6 +7,11 @@
 //
 // Both are bound by memory: append reads the new rows (bf16) and writes their
 // codes, eviction reads the weights of every token and moves the kept rows.
+// Measured: 13,600 tokens of 6 prompts, 8 heads: 20 us (2.8 TB/s; 8.5 us at the
+// measured copy rate); one token for 64 sequences: 7.6 us, a launch and a chain
+// of four reads; 32 sequences of 6,000 to 16,384 tokens to 4,096, 8 heads: 134 us
+// (85 us at the copy rate), 31 us of it the selection, whose instructions bound it,
+// and 105 us the move (5.2 TB/s).
 
 #include "common.cuh"
 #include "e4m3.cuh"
@@ -399,7 +404,7 @@ cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_
   const int most = min(c.max_new, c.rows);
   const int touched = (most + c.block - 2) / c.block + 1;  // blocks that `most` tokens can lie in
   // Single tokens: a CTA per unit, for latency. Prompts: four units a CTA, since most CTAs of a batch of unequal
-  // prompts find nothing to do (6 prompts of 300 to 9,001 tokens: 26 us with one unit, MEASURE with four).
+  // prompts find nothing to do (6 prompts of 300 to 9,001 tokens: 26 us with one unit, 20 us with four).
   const int units = touched > 1 ? 4 : 1;
   const dim3 grid(static_cast<unsigned>(touched) * ((2 * c.H_kv + units - 1) / units), c.B);
   const int threads = c.block * c.d / 8 / kPasses;

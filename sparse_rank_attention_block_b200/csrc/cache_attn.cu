@@ -37,6 +37,12 @@
 // References move, and the output is rescaled, only when a maximum grows by
 // more than 2^8 (exact: every term shares the reference).
 //
+// Measured (32 heads over 8, d = 128): one sequence of 131,072 tokens 52 us
+// (5.2 TB/s; 41 us at the measured copy rate), 64 sequences of 500 to 16,000
+// tokens with weights 137 us (97 us), of which the first kernel takes 117, the
+// join 6, the weights 16. Two CTAs of three stages an SM against three of two:
+// 52.6 and 54.3 us (long), 33.0 and 37.9 us (16 sequences, 4 new tokens).
+//
 // Tokens that a row must not see get a score of -inf; V codes of tokens behind
 // the sequence (free slots, holding anything) are cleared before use.
 
@@ -63,8 +69,8 @@ constexpr int kCtasPerSm = 2;
 constexpr int kSms = 148;
 constexpr int kLeast = 8;      // places of a stretch, at least
 // What a unit costs before its first tile (block numbers, scales, Q, the merge at its end: each a chain of
-// reads), in tiles: places without a tile at its start. attn over 16 sequences of 33 to 6,000 tokens, 4 new
-// tokens each: MEASURE.
+// reads), in tiles: places without a tile at its start. 16 sequences of 33 to 6,000 tokens, 4 new tokens each:
+// 40.9, 37.9, 36.6 and 41.0 us with 4, 8, 16 and 32; 64 sequences of 500 to 16,000: 139.9, 137.7, 140.0, 141.9 us.
 constexpr int kLead = 8;
 constexpr int kWholeTiles = 16;
 constexpr int kMaxSeq = 65536;

@@ -13,21 +13,28 @@
 // same key head (equal work under the causal mask) or, where the heads of a
 // key head are odd in number, two adjacent row tiles of one head.
 //
-// Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 and 2 issue
-// the MMAs of tile 0 and 1 (2 also finds the CTA's tile and owns TMEM), 3 clears V
-// rows behind the sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1,
-// a thread per row. An issuing thread blocks while the tensor pipe is busy, so
-// one for both tiles left the pipe idle through its waits (a pair of steps took
-// 4,020 cycles with one, MEASURE with two).
+// Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 issues every
+// MMA, 2 finds the CTA's tile, 3 owns TMEM and clears V rows behind the
+// sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1, a thread per row.
 //
-// The MMAs of one thread execute in order, so the issue order PV_w(j),
-// QK_w(j+1) lets P_w overlay S_w in TMEM (bf16, half the columns): QK_w(j+1)
-// comes after PV_w(j) has read P_w, and S_w(j+1) ready implies PV_w(j) done, so
-// the softmax may rescale O_w without another wait. P_w is handed over in two
-// halves: the product of the first runs under the exponentials of the second. It does so only when a row's
+// The MMAs of one thread execute in order, so the issue order
+//   PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)
+// lets P_w overlay S_w in TMEM (bf16, half the columns): QK_w(j+1) comes
+// after PV_w(j) has read P_w, and S_w(j+1) ready implies PV_w(j) done, so the
+// softmax may rescale O_w without another wait. It does so only when a row's
 // maximum grows by more than 2^8 (exact: numerator and denominator share the
 // reference). P is rounded to bf16 (the type of V, as the MMA asks); the sum
-// takes the unrounded fp32 values.
+// takes the unrounded fp32 values. One issuer also keeps the two tiles in
+// opposite phase; an issuer for each tile let them fall into step, both in the
+// exponentials and then both in the MMAs (4,230 cycles for a pair of steps).
+// Handing P over in two halves cost more in waits than it overlapped (+4 %), and
+// taking a share of the exponentials on the FMA pipe lost 4 to 8 %.
+//
+// Measured: one sequence of 16,384 tokens, 16 heads over 4, causal: 1.01 ms,
+// 1,080 TFLOP/s (0.67 of the measured burst peak; clocks fall to 1.53 GHz
+// under it), 3,350 cycles for a pair of steps where the tensor pipe alone needs
+// 2,048: each tile's chain of softmax, P V and Q K^T is what remains. Short
+// sequences pay about 5 us per CTA for its start and end, which nothing overlaps.
 //
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+d), O_1 [384,384+d).
 // Shared memory: Q_0, Q_1 (later the output tiles), kStages tiles of K or V.
@@ -73,8 +80,8 @@ struct Smem {
 };
 
 enum {  // w: tile
-  B_QFULL = 0, B_SFULL = 2, B_PHALF = 4, B_PFULL = 6, B_ODONE = 8, B_DRAIN = 10, B_VLAST = 12, B_VCLEAR = 13,
-  B_FULL = 14  // ring full, then ring empty
+  B_QFULL = 0, B_SFULL = 2, B_PFULL = 4, B_ODONE = 6, B_DRAIN = 8, B_VLAST = 9, B_VCLEAR = 10,
+  B_FULL = 11  // ring full, then ring empty
 };
 
 // What the CTA works on, found by one warp.
@@ -234,8 +241,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       tc::mbar_init(&bars[B_SFULL + w], 1);
       tc::mbar_init(&bars[B_PFULL + w], 4);  // a warp each
       tc::mbar_init(&bars[B_ODONE + w], 1);
-      tc::mbar_init(&bars[B_DRAIN + w], 1);
     }
+    tc::mbar_init(&bars[B_DRAIN], 1);
     tc::mbar_init(&bars[B_VLAST], 1);
     tc::mbar_init(&bars[B_VCLEAR], 32);
     for (int s = 0; s < NS; ++s) {
@@ -313,7 +320,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       // ------------------------------------------------------------ MMA issue
       // The whole warp walks the loop, so that descriptors and addresses are uniform values; one lane issues. With
       // one lane in a branch of its own they were moved between register files for every MMA, and the pipe waited
-      // for them (a pair of steps took 3,880 cycles, MEASURE like this).
+      // for them (a pair of steps took 3,880 cycles, 3,350 like this).
       constexpr uint32_t idesc_qk = tc::idesc_bf16(128, 128, false);
       constexpr uint32_t idesc_pv = tc::idesc_bf16(128, D, true);  // B = V, MN-major
       const uint32_t leader = lane == 0;

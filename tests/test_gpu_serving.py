@@ -623,3 +623,84 @@ def test_serving_run_together():
     for _ in range(6):
         lens = [t + 1 for t in lens]
         decode(more, lens, ws2, p2)
+
+
+@pytest.mark.parametrize("call", ["prompt", "cache"])
+def test_wait_that_runs_out_is_reported_and_the_next_call_works(call):
+    """With a limit of 0 a wait gives up unless its phase is already complete: the kernel reports it, drains and
+    ends; afterwards the same call works on the same workspace. (The cache kernel's loads may all have landed before
+    its waits: then nothing runs out, and the output is right.)"""
+    rng = np.random.default_rng(19)
+    if call == "prompt":
+        q, k, v = (bf16((700, h, 128), rng).to(DEV) for h in (4, 2, 2))
+        p = sda.prompt_params(n_seq=2, rows_q=700, rows_k=700, H=4, H_kv=2, d=128)
+        ws, seq, o = sda.Workspace(p), dev(offsets([500, 200])), torch.empty_like(q)
+        run = lambda: sda.sda_prompt_attn_fwd(p, q, k, v, seq, seq, o, None, ws.ptr, ws.nbytes)  # noqa: E731
+    else:
+        c = Cache(rng, [3000, 40], 64, 8, 2, 128, [1, 1])
+        q = bf16((2, 8, 128), rng).to(DEV)
+        ws, o = c.ws, torch.empty_like(q)
+        a = (q, dev(c.seq), *c.args(), None, None, o)
+        run = lambda: sda.sda_cache_attn_fwd(c.p, *a, ws.ptr, ws.nbytes)  # noqa: E731
+    run()
+    ws.check()
+    want = o.clone()
+    before = sda.sda_set_attention_wait_limit_ns(0)
+    try:
+        run()
+        try:
+            ws.check()
+            assert call == "cache" and torch.equal(o, want)
+        except sda.SdaError as e:
+            assert e.code == -7
+    finally:
+        sda.sda_set_attention_wait_limit_ns(before)
+    ws.check()
+    o.zero_()
+    run()
+    ws.check()
+    assert torch.equal(o, want)
+
+
+def test_cache_shared_prefix_and_many_short_sequences():
+    """Blocks shared by sequences (a common prefix), more sequences than a warp has lanes, some without rows, some
+    without tokens; block tables wide enough that the work is split."""
+    rng = np.random.default_rng(20)
+    B, H, H_kv, d, block = 70, 4, 2, 64, 16
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    lens[3], lens[40] = 700, 0
+    new = [int(x) for x in rng.integers(0, 3, B)]
+    c = Cache(rng, lens, block, H, H_kv, d, new, width=64)
+    for b in range(5, 60, 7):                     # the first block of some is that of sequence 3
+        if lens[b]:
+            c.table[b, 0] = c.table[3, 0]
+    q = bf16((int(c.seq[-1]), H, d), rng).to(DEV)
+    o = c.attend(q)
+    c.ws.check()
+    want, spread, _ = O.cache_attention(f64(q), c.seq, c.lens, c.table, block, c.host)
+    size = max(score_size(f64(q), O.cache_values(c.host, "k", c.table[b], t, block, h))
+               for b, t in enumerate(c.lens) if t for h in range(H_kv))
+    assert np.all(np.abs(f64(o) - want) <= attention_tolerance(want, spread, size, d, U_F16))
+
+
+def test_serving_rows_apart():
+    """q, k, v of the cache calls as slices of one projection's rows, o as a slice of a wider tensor."""
+    rng = np.random.default_rng(21)
+    H, H_kv, d, block, lens, new = 4, 2, 64, 16, [50, 33], [2, 1]
+    n = sum(new)
+    rows = bf16((n, (H + 2 * H_kv) * d), rng).to(DEV)
+    q, k, v = (x.unflatten(1, (h, d)) for x, h in zip(rows.split([H * d, H_kv * d, H_kv * d], 1), (H, H_kv, H_kv)))
+    wide = torch.full((n, 2 * H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    ld = rows.shape[1]
+    c = Cache(rng, lens, block, H, H_kv, d, new, ld_q=ld, ld_k=ld, ld_v=ld, ld_o=2 * H * d)
+    O.append(f64(k), f64(v), c.seq, c.lens, c.table, block, c.host)
+    c.append(k, v, w=False)
+    c.check_pool()
+    o = wide[:, H:]
+    sda.sda_cache_attn_fwd(c.p, q, dev(c.seq), *c.args(), None, None, o, c.ws.ptr, c.ws.nbytes)
+    c.ws.check()
+    assert torch.all(wide[:, :H] == 7)
+    want, spread, _ = O.cache_attention(f64(q), c.seq, c.lens, c.table, block, c.host)
+    size = max(score_size(f64(q), O.cache_values(c.host, "k", c.table[b], t, block, h))
+               for b, t in enumerate(lens) for h in range(H_kv))
+    assert np.all(np.abs(f64(o) - want) <= attention_tolerance(want, spread, size, d, U_F16))
