@@ -432,7 +432,8 @@ int32_t sda_cache_evict(const sda_cache_params* p, const int32_t* lens, const in
 /* Failure-detection diagnostic: sets the time limit, in nanoseconds, of the
  * waits on pipeline progress (TMA tiles landed, MMAs done, softmax tiles
  * handed over) in the tcgen05 sparse attention kernel of sda_sparse_attn_fwd
- * and sda_forward, for every launch made after the call, from any thread;
+ * and sda_forward, and in the kernels of sda_prompt_attn_fwd and
+ * sda_cache_attn_fwd, for every launch made after the call, from any thread;
  * returns the previous limit. The default is 2e9 (2 s, far beyond any
  * legitimate wait). 0 makes a wait give up unless its phase is already
  * complete at the first, non-blocking test, so a launch then reliably takes

@@ -55,7 +55,7 @@
 #include "e4m3.cuh"
 #include "launch.cuh"
 #include "serving.h"
-#include "tc.cuh"
+#include "serving_tc.cuh"
 
 namespace sda {
 
@@ -1066,7 +1066,7 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheLayout& y, void* ws, co
   a.tile_rows = y.tile_rows;
   a.whole_row_tiles = y.whole_row_tiles;
   a.rows_pad = y.rows_pad;
-  a.wait_ns = attention_wait_limit();
+  a.wait_ns = serving_wait_limit();
   if (c.d == 128) return run<128>(c, a, k_codes, v_codes, w_in, w_out, stream);
   if (c.d == 64) return run<64>(c, a, k_codes, v_codes, w_in, w_out, stream);
   return cudaErrorInvalidValue;

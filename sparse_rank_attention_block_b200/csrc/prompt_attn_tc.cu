@@ -55,7 +55,7 @@
 #include "ex2_fma.cuh"
 #include "launch.cuh"
 #include "serving.h"
-#include "tc.cuh"
+#include "serving_tc.cuh"
 
 namespace sda {
 
@@ -179,33 +179,6 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
     if (rest < all) break;
     rest -= all;
   }
-}
-
-// tcgen05.mma and commit for a whole warp: the lane with `leader` != 0 issues.
-__device__ __forceinline__ void mma_ss_by(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_by(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void commit_by(uint32_t leader, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      ::"r"(smem_u32(bar)), "r"(leader)
-      : "memory");
 }
 
 __device__ __forceinline__ uint32_t sw(uint32_t row, uint32_t chunk) { return tc::sw128_offset(row, chunk); }
@@ -336,15 +309,15 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t at = kk / 4 * kHalf16 + kk % 4 * 2;
-          mma_ss_by(leader, tmem + kColS + 128 * w, da + at, db + at, idesc_qk, kk > 0 ? 1u : 0u);
+          tc::mma_ss_by(leader, tmem + kColS + 128 * w, da + at, db + at, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        commit_by(leader, &bars[B_SFULL + w]);
+        tc::commit_by(leader, &bars[B_SFULL + w]);
       };
       auto pv = [&](int w, int st, uint32_t acc) {
         const uint64_t db = desc_v0 + st * kTile16;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts_by(leader, tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db + kk * 128, idesc_pv,
+          tc::mma_ts_by(leader, tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db + kk * 128, idesc_pv,
                     kk > 0 ? 1u : acc);
       };
       if (n > 0) ok = wait(&full[0], 0);
@@ -358,7 +331,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc::fence_after_sync();
         if (ok) qk(1, 0);
       }
-      if (ok && n > 0) commit_by(leader, &empty[0]);
+      if (ok && n > 0) tc::commit_by(leader, &empty[0]);
       int sv = 1, v_par = 0, sk = 2, k_par = 0;  // stages and parities of V_j and K_{j+1}
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
@@ -373,19 +346,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           if (!ok) break;
           tc::fence_after_sync();
           pv(w, sv, j > 0);
-          if (j == nw - 1) commit_by(leader, &bars[B_ODONE + w]);
+          if (j == nw - 1) tc::commit_by(leader, &bars[B_ODONE + w]);
           else qk(w, sk);
         }
         if (!ok) break;
-        commit_by(leader, &empty[sv]);
-        if (j + 1 < n) commit_by(leader, &empty[sk]);
+        tc::commit_by(leader, &empty[sv]);
+        if (j + 1 < n) tc::commit_by(leader, &empty[sk]);
         sv += 2;
         if (sv >= NS) sv -= NS, v_par ^= 1;
         sk += 2;
         if (sk >= NS) sk -= NS, k_par ^= 1;
       }
       // drain: every MMA this warp issued
-      commit_by(leader, &bars[B_DRAIN]);
+      tc::commit_by(leader, &bars[B_DRAIN]);
       tc::wait_warp(&bars[B_DRAIN], 0, &never);
     } else if (warp == 3 && n > 0) {
       // ------------------------------------------------------------ V rows behind the sequence
@@ -620,7 +593,7 @@ cudaError_t run(const Prompt& p, const uint16_t* q, const uint16_t* k, const uin
   const long long tiles = static_cast<long long>(p.rows_q) / R + p.n_seq;  // at least the sequences' row tiles
   const long long blocks = tiles * (pair_heads ? p.H / 2 : p.H);
   return launch_after(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, mq, mk, mv, p,
-                      pair_heads, seq_q, seq_k, o, lse, status, attention_wait_limit());
+                      pair_heads, seq_q, seq_k, o, lse, status, serving_wait_limit());
 }
 
 }  // namespace

@@ -19,9 +19,12 @@ struct Prompt {
   float scale_log2;                  // softmax scale * log2(e)
 };
 
+// serving_api.cu
+// Limit of the serving kernels' waits, as sda_set_attention_wait_limit_ns sets it.
+uint64_t serving_wait_limit();
+void set_serving_wait_limit(uint64_t limit_ns);
+
 // prompt_attn_tc.cu
-// Waits keep the limit of sda_set_attention_wait_limit_ns (attention_wait_limit).
-uint64_t attention_wait_limit();
 cudaError_t launch_prompt_attn(const Prompt& p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                const int32_t* seq_q, const int32_t* seq_k, uint16_t* o, float* lse, unsigned* status,
                                cudaStream_t stream);

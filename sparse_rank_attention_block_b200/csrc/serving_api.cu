@@ -1,6 +1,7 @@
 // Host side of the serving operators' C entry points (include/sda.h): argument
 // checks, workspace layout, launches. No device memory is allocated here.
 
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -161,7 +162,14 @@ int32_t need_rows(const Cache& C) {
   return SDA_OK;
 }
 
+std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};  // 2 s: far beyond any legitimate wait
+
 }  // namespace
+
+namespace sda {
+uint64_t serving_wait_limit() { return g_wait_limit_ns.load(); }
+void set_serving_wait_limit(uint64_t limit_ns) { g_wait_limit_ns.store(limit_ns); }
+}  // namespace sda
 
 extern "C" {
 

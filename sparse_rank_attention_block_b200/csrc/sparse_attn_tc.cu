@@ -56,7 +56,6 @@
 #include "common.cuh"
 #include "ex2_fma.cuh"
 #include "kernels.h"
-#include "serving.h"
 #include "tc.cuh"
 
 namespace sda {
@@ -891,7 +890,6 @@ cudaError_t run_tc(const Problem& P, const uint16_t* q, const uint16_t* k, const
 }  // namespace
 
 uint64_t set_attention_wait_limit(uint64_t limit_ns) { return g_wait_limit_ns.exchange(limit_ns); }
-uint64_t attention_wait_limit() { return g_wait_limit_ns.load(); }
 
 bool sparse_attn_tc_supported(const Problem& P) {
   return (P.block_q == kBQ || P.block_q == kBQ / 2) && P.block_k == kBK && (P.d == 64 || P.d == 128);
