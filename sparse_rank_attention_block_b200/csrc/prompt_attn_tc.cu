@@ -34,7 +34,9 @@
 // 1,080 TFLOP/s (0.67 of the measured burst peak; clocks fall to 1.53 GHz
 // under it), 3,350 cycles for a pair of steps where the tensor pipe alone needs
 // 2,048: each tile's chain of softmax, P V and Q K^T is what remains. Short
-// sequences pay about 5 us per CTA for its start and end, which nothing overlaps.
+// sequences pay about 5 us per CTA for its start and end, which nothing overlaps:
+// the search for the tile 1.3 us, the first loads and scores 1.8 us, the output 2 us
+// (all SMs read and write in bursts); a step takes 2.2 us.
 //
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+d), O_1 [384,384+d).
 // Shared memory: Q_0, Q_1 (later the output tiles), kStages tiles of K or V.
@@ -112,15 +114,15 @@ __device__ __forceinline__ int keys_below(const Prompt& p, const Span& s, int en
   return p.causal ? max(0, min(s.nk, end + s.nk - s.nq)) : s.nk;
 }
 
-// Row tiles (of R rows) of a sequence whose key steps number more than x.
-__device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int R, int x) {
-  const int T = (s.nq + R - 1) / R;
+// Row tiles (of R = 2^lr rows) of a sequence whose key steps number more than x.
+__device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int lr, int x) {
+  const int T = (s.nq + (1 << lr) - 1) >> lr;
   if (x < 0) return T;
   if (!p.causal) return s.nk > kTile * x ? T : 0;
   if (s.nk <= kTile * x) return 0;  // the last tile sees all nk keys, none sees more
   // tile t (not the last) sees (t + 1) R + nk - nq keys
   const int need = kTile * x - (s.nk - s.nq);
-  const int first = need < 0 ? 0 : need / R;
+  const int first = need < 0 ? 0 : need >> lr;
   return T - min(first, T - 1);
 }
 
@@ -128,14 +130,14 @@ __device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int R,
 // the last ones to start are short: tile i of the order has the step count x
 // with over(x) <= i < over(x - 1), over(x) the number of tiles of more than x
 // steps, found by bisection; among equals, sequences in order.
-__device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int R, int i, Item* out,
+__device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int lr, int i, Item* out,
                           bool& bad) {
   const int lane = threadIdx.x & 31;
   Span mine{0, 0, 0, 0};
   if (lane < p.n_seq) mine = span_of(p, seq_q, seq_k, lane, bad);
   auto over = [&](int x) {
-    int n = lane < p.n_seq ? tiles_over(p, mine, R, x) : 0;
-    for (int s = 32 + lane; s < p.n_seq; s += 32) n += tiles_over(p, span_of(p, seq_q, seq_k, s, bad), R, x);
+    int n = lane < p.n_seq ? tiles_over(p, mine, lr, x) : 0;
+    for (int s = 32 + lane; s < p.n_seq; s += 32) n += tiles_over(p, span_of(p, seq_q, seq_k, s, bad), lr, x);
     return __reduce_add_sync(0xffffffffu, n);
   };
   int top = lane < p.n_seq ? mine.nk : 0;
@@ -143,7 +145,7 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   top = __reduce_max_sync(0xffffffffu, top);
   out->valid = 0;
   if (p.n_seq == 1) {  // one sequence: its tiles from the last
-    const int T = (mine.nq + R - 1) / R;
+    const int T = (mine.nq + (1 << lr) - 1) >> lr;
     if (lane == 0 && i < T) *out = Item{1, mine.q0, mine.nq, mine.k0, mine.nk, T - 1 - i};
     return;
   }
@@ -159,8 +161,8 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
     const int s = base + lane;
     Span sp = base == 0 ? mine : Span{0, 0, 0, 0};
     if (base > 0 && s < p.n_seq) sp = span_of(p, seq_q, seq_k, s, bad);
-    const int above = s < p.n_seq ? tiles_over(p, sp, R, lo) : 0;
-    const int n = s < p.n_seq ? tiles_over(p, sp, R, lo - 1) - above : 0;
+    const int above = s < p.n_seq ? tiles_over(p, sp, lr, lo) : 0;
+    const int n = s < p.n_seq ? tiles_over(p, sp, lr, lo - 1) - above : 0;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -172,7 +174,7 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
       out->nq = sp.nq;
       out->k0 = sp.k0;
       out->nk = sp.nk;
-      out->t = (sp.nq + R - 1) / R - 1 - above - (rest - (sum - n));
+      out->t = ((sp.nq + (1 << lr) - 1) >> lr) - 1 - above - (rest - (sum - n));
       out->valid = 1;
     }
     const int all = __shfl_sync(0xffffffffu, sum, 31);
@@ -235,7 +237,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile unsigned*>(status) & kStatusTimeout) ? 1 : 0;
   if (warp == 2) {
     bool bad = false;
-    find_item(p, seq_q, seq_k, R, blockIdx.x / groups, item, bad);
+    find_item(p, seq_q, seq_k, pair_heads ? 7 : 8, blockIdx.x / groups, item, bad);
     if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report_status(status, kStatusBadIndex);
   }
   __syncthreads();
