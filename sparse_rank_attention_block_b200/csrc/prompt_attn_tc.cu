@@ -51,6 +51,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <mutex>
 
 #include "common.cuh"
@@ -65,6 +66,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kTile = 128;  // query rows of a tile, keys of a step
+constexpr int kSms = 148;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * tile
 constexpr int kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
@@ -74,17 +76,19 @@ template <int D>
 struct Smem {
   static constexpr int kHalves = D / 64;
   static constexpr int kTileBytes = kHalves * kTile * 128;  // [half][128 rows][128 B]
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + 2 * kTileBytes;
-  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kOut = kRing + kStages * kTileBytes;  // 32 rows x 128 B for each softmax warp
+  static constexpr int kBars = kOut + 8 * 4096;
   static constexpr int kTotal = kBars + 512;
 };
 
-enum {  // w: tile
-  B_QFULL = 0, B_SFULL = 2, B_PFULL = 4, B_ODONE = 6, B_DRAIN = 8, B_VLAST = 9, B_VCLEAR = 10,
-  B_FULL = 11  // ring full, then ring empty
+enum {  // w: tile (two each); an item's barriers two each, by its number
+  B_QFULL = 0, B_QFREE = 2, B_SFULL = 4, B_PFULL = 6, B_ODONE = 8, B_OFREE = 10, B_ITEM = 12, B_TAKEN = 14, B_DRAIN = 16,
+  B_FULL = 17  // ring full, then ring empty
 };
+constexpr int kConsumers = 10;  // of an item: loader, MMA warp, 8 softmax warps
 
 // What the CTA works on, found by one warp.
 struct Item {
@@ -202,24 +206,24 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   unsigned char* tail = smem + S::kBars + 8 * (B_FULL + 2 * NS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 4);
-  Item* item = reinterpret_cast<Item*>(tail + 16);
+  Item* items = reinterpret_cast<Item*>(tail + 16);  // two
 
   // through a shuffle, so that the compiler knows it to be the same for the warp
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int groups = pair_heads ? p.H / 2 : p.H;  // head groups, fastest: they share the tile's K and V through L2
-  const int hg = blockIdx.x % groups;
-  const int R = pair_heads ? kTile : 2 * kTile;
 
   if (threadIdx.x == 0) {
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&bars[B_QFULL + w], 1);
+      tc::mbar_init(&bars[B_QFREE + w], 1);
       tc::mbar_init(&bars[B_SFULL + w], 1);
       tc::mbar_init(&bars[B_PFULL + w], 4);  // a warp each
       tc::mbar_init(&bars[B_ODONE + w], 1);
+      tc::mbar_init(&bars[B_OFREE + w], 4);
+      tc::mbar_init(&bars[B_ITEM + w], 1);
+      tc::mbar_init(&bars[B_TAKEN + w], kConsumers);
     }
     tc::mbar_init(&bars[B_DRAIN], 1);
-    tc::mbar_init(&bars[B_VLAST], 1);
-    tc::mbar_init(&bars[B_VCLEAR], 32);
     for (int s = 0; s < NS; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -235,62 +239,89 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
   }
   pdl_wait();
   if (threadIdx.x == 0) *abort_flag = (*reinterpret_cast<volatile unsigned*>(status) & kStatusTimeout) ? 1 : 0;
-  if (warp == 2) {
-    bool bad = false;
-    find_item(p, seq_q, seq_k, pair_heads ? 7 : 8, blockIdx.x / groups, item, bad);
-    if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) report_status(status, kStatusBadIndex);
-  }
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  if (*abort_flag || !item->valid) {  // uniform
+  if (*abort_flag) {  // uniform
     if (warp == 3) tc::tmem_dealloc(tmem, kTmemCols);
     return;
   }
 
-  const Span seq{item->q0, item->nq, item->k0, item->nk};
-  const int row0 = item->t * R;
-  const int h0 = pair_heads ? 2 * hg : hg;
-  const int h_kv = h0 / (p.H / p.H_kv);
-  // tile w: rows [row_w, end_w) of the sequence, head h_w, steps n_w (0: nothing visible)
-  const int row_1 = pair_heads ? row0 : row0 + kTile;
-  const int end_0 = min(row0 + kTile, seq.nq), end_1 = min(row_1 + kTile, seq.nq);
-  const bool live_1 = row_1 < seq.nq;
-  const int n0 = (keys_below(p, seq, end_0) + kTile - 1) / kTile;
-  const int n1 = live_1 ? (keys_below(p, seq, end_1) + kTile - 1) / kTile : 0;
-  const int n = __shfl_sync(0xffffffffu, max(n0, n1), 0);
+  // Item r of this CTA: the items go out in rounds, every second one in reverse, so that each CTA's share is even.
+  auto number = [&](int r) {
+    const int c = (r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    return static_cast<long long>(r) * gridDim.x + c;
+  };
+  // What a role needs to know of item r: waits for it, copies it, hands its place back.
+  struct Work {
+    Span seq;
+    int row0, row_1, n0, n1, n, h0;
+    bool live_1;
+  };
+  bool ok = true;
+  auto take = [&](int r, Work& k) {  // a whole warp
+    ok = tc::wait_warp(&bars[B_ITEM + (r & 1)], (r >> 1) & 1, abort_flag, wait_ns);
+    if (!ok) return false;
+    const Item it = items[r & 1];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bars[B_TAKEN + (r & 1)]);
+    if (!it.valid) return false;
+    const int hg = static_cast<int>(number(r) % groups);
+    k.seq = Span{it.q0, it.nq, it.k0, it.nk};
+    k.row0 = it.t * (pair_heads ? kTile : 2 * kTile);
+    k.h0 = pair_heads ? 2 * hg : hg;
+    // tile w: rows [row_w, end_w) of the sequence, head h_w, steps n_w (0: nothing visible)
+    k.row_1 = pair_heads ? k.row0 : k.row0 + kTile;
+    k.live_1 = k.row_1 < it.nq;
+    k.n0 = (keys_below(p, k.seq, min(k.row0 + kTile, it.nq)) + kTile - 1) / kTile;
+    k.n1 = k.live_1 ? (keys_below(p, k.seq, min(k.row_1 + kTile, it.nq)) + kTile - 1) / kTile : 0;
+    k.n = max(k.n0, k.n1);
+    return true;
+  };
+  const int g = p.H / p.H_kv;
+  Work k;
 
   if (warp < 4) {
     tc::setmaxnreg_dec<kRegsLow>();
     volatile int never = 0;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ------------------------------------------------------------ loads
-      bool ok = true;
-      for (int w = 0; w < 2; ++w) {
-        if ((w ? n1 : n0) == 0) continue;
-        tc::mbar_arrive_expect_tx(&bars[B_QFULL + w], S::kTileBytes);
-        for (int hf = 0; hf < S::kHalves; ++hf)
-          tc::tma_load_3d(smem + S::kQ + w * S::kTileBytes + hf * kTile * 128, &tm_q, &bars[B_QFULL + w], 64 * hf,
-                          pair_heads ? h0 + w : h0, seq.q0 + (w ? row_1 : row0));
-      }
-      // ring order K_0, V_0, K_1, V_1, ...: the order in which the MMAs release them
-      int c = 0;
-      for (; c < 2 * n; ++c) {
-        const int st = c % NS;
-        if (c >= NS) ok = tc::wait1(&empty[st], (c / NS - 1) & 1, abort_flag, wait_ns);
+      int cnt = 0;                  // ring tiles so far
+      int q_cnt[2] = {0, 0};        // Q tiles so far
+      for (int r = 0; take(r, k); ++r) {
+        if (lane == 0) {
+          for (int w = 0; w < 2 && ok; ++w) {
+            if ((w ? k.n1 : k.n0) == 0) continue;
+            if (q_cnt[w] > 0) ok = tc::wait1(&bars[B_QFREE + w], (q_cnt[w] - 1) & 1, abort_flag, wait_ns);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(&bars[B_QFULL + w], S::kTileBytes);
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tc::tma_load_3d(smem + S::kQ + w * S::kTileBytes + hf * kTile * 128, &tm_q, &bars[B_QFULL + w], 64 * hf,
+                              pair_heads ? k.h0 + w : k.h0, k.seq.q0 + (w ? k.row_1 : k.row0));
+            ++q_cnt[w];
+          }
+          // ring order K_0, V_0, K_1, V_1, ...: the order in which the MMAs release them
+          for (int c = 0; c < 2 * k.n && ok; ++c) {
+            const int st = cnt % NS;
+            if (cnt >= NS) ok = tc::wait1(&empty[st], (cnt / NS - 1) & 1, abort_flag, wait_ns);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(&full[st], S::kTileBytes);
+            for (int hf = 0; hf < S::kHalves; ++hf)
+              tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + hf * kTile * 128, c % 2 == 0 ? &tm_k : &tm_v, &full[st],
+                              64 * hf, k.h0 / g, k.seq.k0 + c / 2 * kTile);
+            ++cnt;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0);
         if (!ok) break;
-        // the last V tile has a barrier of its own: another warp waits for it, from the start
-        uint64_t* bar = c == 2 * n - 1 ? &bars[B_VLAST] : &full[st];
-        tc::mbar_arrive_expect_tx(bar, S::kTileBytes);
-        for (int hf = 0; hf < S::kHalves; ++hf)
-          tc::tma_load_3d(smem + S::kRing + st * S::kTileBytes + hf * kTile * 128, c % 2 == 0 ? &tm_k : &tm_v, bar,
-                          64 * hf, h_kv, seq.k0 + c / 2 * kTile);
       }
       // no load is in flight when the CTA ends, whatever the others did
-      for (int w = 0; w < 2; ++w)
-        if ((w ? n1 : n0) > 0) tc::wait1(&bars[B_QFULL + w], 0, &never);
-      for (int b = c > NS ? c - NS : 0; b < c; ++b)
-        tc::wait1(b == 2 * n - 1 ? &bars[B_VLAST] : &full[b % NS], b == 2 * n - 1 ? 0 : (b / NS) & 1, &never);
+      if (lane == 0) {
+        for (int w = 0; w < 2; ++w)
+          if (q_cnt[w] > 0) tc::wait1(&bars[B_QFULL + w], (q_cnt[w] - 1) & 1, &never);
+        for (int b = cnt > NS ? cnt - NS : 0; b < cnt; ++b) tc::wait1(&full[b % NS], (b / NS) & 1, &never);
+      }
+      __syncwarp();
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issue
       // The whole warp walks the loop, so that descriptors and addresses are uniform values; one lane issues. With
@@ -299,12 +330,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       constexpr uint32_t idesc_qk = tc::idesc_bf16(128, 128, false);
       constexpr uint32_t idesc_pv = tc::idesc_bf16(128, D, true);  // B = V, MN-major
       const uint32_t leader = lane == 0;
-      const int m0 = __shfl_sync(0xffffffffu, n0, 0), m1 = __shfl_sync(0xffffffffu, n1, 0);
       const uint64_t desc_k0 = tc::smem_desc_sw128(smem + S::kRing, 16, 1024);           // K: K-major
       const uint64_t desc_v0 = tc::smem_desc_sw128(smem + S::kRing, kTile * 128, 1024);  // V: MN-major
       const uint64_t desc_q0 = tc::smem_desc_sw128(smem + S::kQ, 16, 1024);
       constexpr uint32_t kTile16 = S::kTileBytes / 16, kHalf16 = kTile * 128 / 16;       // descriptors count in 16 bytes
-      bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::wait_warp(bar, parity, abort_flag, wait_ns); };
       auto qk = [&](int w, int st) {
         const uint64_t da = desc_q0 + w * kTile16, db = desc_k0 + st * kTile16;
@@ -320,62 +349,98 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           tc::mma_ts_by(leader, tmem + kColO + 128 * w, tmem + kColS + 128 * w + kk * 8, db + kk * 128, idesc_pv,
-                    kk > 0 ? 1u : acc);
+                        kk > 0 ? 1u : acc);
       };
-      if (n > 0) ok = wait(&full[0], 0);
-      if (ok && m0 > 0) {
-        ok = wait(&bars[B_QFULL], 0);
-        tc::fence_after_sync();
-        if (ok) qk(0, 0);
-      }
-      if (ok && m1 > 0) {
-        ok = wait(&bars[B_QFULL + 1], 0);
-        tc::fence_after_sync();
-        if (ok) qk(1, 0);
-      }
-      if (ok && n > 0) tc::commit_by(leader, &empty[0]);
-      int sv = 1, v_par = 0, sk = 2, k_par = 0;  // stages and parities of V_j and K_{j+1}
-#pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        ok = j == n - 1 ? wait(&bars[B_VCLEAR], 0) : wait(&full[sv], v_par);
-        if (ok && j + 1 < n) ok = wait(&full[sk], k_par);
-        if (!ok) break;
+      // place in the ring of the next tile, its stage and parity; counts of each tile's items and steps so far
+      int st = 0, par = 0;
+      uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0}, o_cnt[2] = {0, 0};
+      auto advance = [&](int& s_, int& p_, int by) {
+        s_ += by;
+        if (s_ >= NS) s_ -= NS, p_ ^= 1;
+      };
+      for (int r = 0; take(r, k); ++r) {
+        const int n = __shfl_sync(0xffffffffu, k.n, 0), m0 = __shfl_sync(0xffffffffu, k.n0, 0),
+                  m1 = __shfl_sync(0xffffffffu, k.n1, 0);
+        if (n == 0) continue;
+        ok = wait(&full[st], par);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const int nw = w ? m1 : m0;
-          if (j >= nw) continue;
-          ok = wait(&bars[B_PFULL + w], j & 1);
-          if (!ok) break;
+          if (!ok || (w ? m1 : m0) == 0) continue;
+          ok = wait(&bars[B_QFULL + w], q_par[w]);
+          q_par[w] ^= 1;
           tc::fence_after_sync();
-          pv(w, sv, j > 0);
-          if (j == nw - 1) tc::commit_by(leader, &bars[B_ODONE + w]);
-          else qk(w, sk);
+          if (ok) {
+            qk(w, st);
+            if ((w ? m1 : m0) == 1) tc::commit_by(leader, &bars[B_QFREE + w]);
+          }
         }
         if (!ok) break;
-        tc::commit_by(leader, &empty[sv]);
-        if (j + 1 < n) tc::commit_by(leader, &empty[sk]);
-        sv += 2;
-        if (sv >= NS) sv -= NS, v_par ^= 1;
-        sk += 2;
-        if (sk >= NS) sk -= NS, k_par ^= 1;
+        tc::commit_by(leader, &empty[st]);
+        advance(st, par, 1);
+        int sv = st, v_par = par, sk = st, k_par = par;  // V_j and K_{j+1}
+        advance(sk, k_par, 1);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          ok = wait(&full[sv], v_par);
+          if (ok && j + 1 < n) ok = wait(&full[sk], k_par);
+          if (!ok) break;
+          const int there = k.seq.nk - j * kTile;
+          if (there < kTile) {  // the last tile: clear the V rows behind the sequence
+            unsigned char* vst = smem + S::kRing + sv * S::kTileBytes;
+            for (int e = there * 8 * S::kHalves + lane; e < kTile * 8 * S::kHalves; e += 32) {
+              const int row = e / (8 * S::kHalves), ch = e % (8 * S::kHalves);
+              *reinterpret_cast<uint4*>(vst + (ch / 8) * kTile * 128 + row * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int nw = w ? m1 : m0;
+            if (j >= nw) continue;
+            if (j == 0 && o_cnt[w] > 0) ok = wait(&bars[B_OFREE + w], (o_cnt[w] - 1) & 1);  // the last item's output is out
+            if (ok) ok = wait(&bars[B_PFULL + w], p_par[w]);
+            if (!ok) break;
+            p_par[w] ^= 1;
+            tc::fence_after_sync();
+            pv(w, sv, j > 0);
+            if (j == nw - 1) {
+              tc::commit_by(leader, &bars[B_ODONE + w]);
+              ++o_cnt[w];
+            } else {
+              qk(w, sk);
+              if (j + 1 == nw - 1) tc::commit_by(leader, &bars[B_QFREE + w]);
+            }
+          }
+          if (!ok) break;
+          tc::commit_by(leader, &empty[sv]);
+          if (j + 1 < n) tc::commit_by(leader, &empty[sk]);
+          advance(sv, v_par, 2);
+          advance(sk, k_par, 2);
+        }
+        if (!ok) break;
+        advance(st, par, 0);
+        // 2 n tiles of the item, one of them taken above
+        for (int left = 2 * n - 1; left > 0; left -= NS) advance(st, par, left < NS ? left : NS);
       }
       // drain: every MMA this warp issued
       tc::commit_by(leader, &bars[B_DRAIN]);
       tc::wait_warp(&bars[B_DRAIN], 0, &never);
-    } else if (warp == 3 && n > 0) {
-      // ------------------------------------------------------------ V rows behind the sequence
-      const int c = 2 * n - 1;  // the last V tile
-      const bool ok = tc::wait_warp(&bars[B_VLAST], 0, abort_flag, wait_ns);
-      const int valid = seq.nk - (n - 1) * kTile;
-      if (ok && valid < kTile) {
-        unsigned char* vst = smem + S::kRing + (c % NS) * S::kTileBytes;
-        for (int e = valid * 8 * S::kHalves + lane; e < kTile * 8 * S::kHalves; e += 32) {
-          const int row = e / (8 * S::kHalves), ch = e % (8 * S::kHalves);
-          *reinterpret_cast<uint4*>(vst + (ch / 8) * kTile * 128 + row * 128 + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        tc::fence_proxy_async_smem();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ items, one ahead of their use
+      for (int r = 0;; ++r) {
+        if (r >= 2) ok = tc::wait_warp(&bars[B_TAKEN + (r & 1)], ((r >> 1) - 1) & 1, abort_flag, wait_ns);
+        if (!ok) break;
+        bool bad = false;
+        const long long tile = number(r) / groups;
+        find_item(p, seq_q, seq_k, pair_heads ? 7 : 8, static_cast<int>(min(tile, static_cast<long long>(INT_MAX))),
+                  &items[r & 1], bad);
+        if (r == 0 && blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) report_status(status, kStatusBadIndex);
+        __syncwarp();
+        const int valid = *reinterpret_cast<volatile int*>(&items[r & 1].valid);
+        if (lane == 0) tc::mbar_arrive(&bars[B_ITEM + (r & 1)]);
+        if (!valid) break;
       }
-      tc::mbar_arrive(&bars[B_VCLEAR]);
     }
   } else {
     tc::setmaxnreg_inc<kRegsHigh>();
@@ -386,16 +451,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t t_s = tmem + lane_base + kColS + 128 * w;
     const uint32_t t_o = tmem + lane_base + kColO + 128 * w;
-    const int nw = w ? n1 : n0;
-    const int tile_row = w ? row_1 : row0;
+    uint32_t s_par = 0, o_par = 0;  // parities of S and O
+    for (int r = 0; take(r, k); ++r) {
+    const Span seq = k.seq;
+    const int nw = w ? k.n1 : k.n0;
+    const int tile_row = w ? k.row_1 : k.row0;
     const int my_row = tile_row + row;               // row of the sequence
     const int lim = keys_below(p, seq, my_row + 1);  // keys this row sees (rows behind the sequence: all)
     const int lim_first = keys_below(p, seq, tile_row + 1);
-    bool ok = true;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < nw; ++j) {
-      ok = tc::wait_warp(&bars[B_SFULL + w], j & 1, abort_flag, wait_ns);
+      ok = tc::wait_warp(&bars[B_SFULL + w], s_par, abort_flag, wait_ns);
       if (!ok) break;
+      s_par ^= 1;
       tc::fence_after_sync();
       float s[128];
       {
@@ -481,51 +549,60 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars[B_PFULL + w]);
     }
-    const bool live = w == 0 || live_1;
-    if (ok && nw > 0) ok = tc::wait_warp(&bars[B_ODONE + w], 0, abort_flag, wait_ns);
-    if (ok && live) {
+    if (!ok) break;
+    const bool live = w == 0 || k.live_1;
+    if (nw > 0) {
+      ok = tc::wait_warp(&bars[B_ODONE + w], o_par, abort_flag, wait_ns);
+      if (!ok) break;
+      o_par ^= 1;
+    }
+    if (live) {
       tc::fence_after_sync();
-      const int head = pair_heads ? h0 + w : h0;
+      const int head = pair_heads ? k.h0 + w : k.h0;
       const bool mine = my_row < seq.nq;
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
       if (lse != nullptr && mine)
         lse[static_cast<size_t>(seq.q0 + my_row) * p.H + head] =
             l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      // O / l as bf16 into this warp's 32 rows of the (now free) Q tile, then whole rows out
-      unsigned char* otile = smem + S::kQ + w * S::kTileBytes;
+      // O / l as bf16, 64 channels at a time, through this warp's 32 x 128 B, then whole rows out
+      unsigned char* out = smem + S::kOut + (warp - 4) * 4096;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
+      for (int hf = 0; hf < S::kHalves; ++hf) {
+        uint32_t x[64];
         if (nw > 0) {
-          tc::tmem_ld32(t_o + 32 * c, r);
+          tc::tmem_ld32p(t_o + 64 * hf, x);
+          tc::tmem_ld32p(t_o + 64 * hf + 32, x + 32);
           tc::tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
+          for (int e = 0; e < 64; ++e) x[e] = 0u;
+        }
+        if (hf == S::kHalves - 1 && nw > 0) {  // O_w is in registers: the next item may overwrite it
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars[B_OFREE + w]);
         }
 #pragma unroll
-        for (int q8 = 0; q8 < 4; ++q8) {
+        for (int ch = 0; ch < 8; ++ch) {
           uint32_t v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] = pack_bf16(__uint_as_float(r[8 * q8 + 2 * e]) * inv, __uint_as_float(r[8 * q8 + 2 * e + 1]) * inv);
-          const int ch = 4 * c + q8;
-          *reinterpret_cast<uint4*>(otile + (ch / 8) * (kTile * 128) + sw(row, ch % 8)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
+            v[e] = pack_bf16(__uint_as_float(x[8 * ch + 2 * e]) * inv, __uint_as_float(x[8 * ch + 2 * e + 1]) * inv);
+          *reinterpret_cast<uint4*>(out + sw(lane, ch)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-      }
-      __syncwarp();
-      constexpr int kLanes = D / 8;         // lanes that carry a row
-      constexpr int kRows = 32 / kLanes;    // rows per instruction
-      const int ch = lane % kLanes;
-#pragma unroll 4
-      for (int i = 0; i < 32; i += kRows) {
-        const int r = 32 * quarter + i + lane / kLanes;
-        if (tile_row + r < seq.nq) {
-          const uint4 v = *reinterpret_cast<const uint4*>(otile + (ch / 8) * (kTile * 128) + sw(r, ch % 8));
-          *reinterpret_cast<uint4*>(o + static_cast<size_t>(seq.q0 + tile_row + r) * p.ld_o + head * D + 8 * ch) = v;
+        __syncwarp();
+        const int ch = lane % 8;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int rr = i + lane / 8, at = tile_row + 32 * quarter + rr;
+          if (at < seq.nq) {
+            const uint4 v = *reinterpret_cast<const uint4*>(out + sw(rr, ch));
+            *reinterpret_cast<uint4*>(o + static_cast<size_t>(seq.q0 + at) * p.ld_o + head * D + 64 * hf + 8 * ch) = v;
+          }
         }
+        __syncwarp();
       }
+    }
     }
   }
 
@@ -593,7 +670,7 @@ cudaError_t run(const Prompt& p, const uint16_t* q, const uint16_t* k, const uin
   const int pair_heads = (p.H / p.H_kv) % 2 == 0 ? 1 : 0;
   const int R = pair_heads ? kTile : 2 * kTile;
   const long long tiles = static_cast<long long>(p.rows_q) / R + p.n_seq;  // at least the sequences' row tiles
-  const long long blocks = tiles * (pair_heads ? p.H / 2 : p.H);
+  const long long blocks = min(tiles * (pair_heads ? p.H / 2 : p.H), static_cast<long long>(kSms));
   return launch_after(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, mq, mk, mv, p,
                       pair_heads, seq_q, seq_k, o, lse, status, serving_wait_limit());
 }
