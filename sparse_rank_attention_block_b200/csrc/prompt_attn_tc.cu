@@ -14,8 +14,14 @@
 // key head are odd in number, two adjacent row tiles of one head.
 //
 // Warps: 0 loads (TMA: Q tiles, then a ring of K and V tiles), 1 issues every
-// MMA, 2 finds the CTA's tile, 3 owns TMEM and clears V rows behind the
-// sequence; 4..7 and 8..11 softmax and epilogue of tile 0 and 1, a thread per row.
+// MMA and clears V rows behind the sequence, 2 finds the next tiles to work on, 3
+// owns TMEM; 4..7 and 8..11 softmax and epilogue of tile 0 and 1, a thread per row.
+//
+// A CTA takes its share of the (row tile, head group) items one after another, at
+// most one CTA per SM: the search for an item, its loads and its first scores run
+// under the end of the one before (9 prompts of 1 to 2,900 tokens 135 us against
+// 145 us with a CTA per item, 4,680 rows on 512 keys 60 against 70 us; one long
+// sequence loses 3 %, 100 tokens 1.3 us). Items go out heaviest first, in rounds.
 //
 // The MMAs of one thread execute in order, so the issue order
 //   PV_0(j), QK_0(j+1), PV_1(j), QK_1(j+1)
@@ -30,16 +36,13 @@
 // Handing P over in two halves cost more in waits than it overlapped (+4 %), and
 // taking a share of the exponentials on the FMA pipe lost 4 to 8 %.
 //
-// Measured: one sequence of 16,384 tokens, 16 heads over 4, causal: 1.01 ms,
-// 1,080 TFLOP/s (0.67 of the measured burst peak; clocks fall to 1.53 GHz
-// under it), 3,350 cycles for a pair of steps where the tensor pipe alone needs
-// 2,048: each tile's chain of softmax, P V and Q K^T is what remains. Short
-// sequences pay about 5 us per CTA for its start and end, which nothing overlaps:
-// the search for the tile 1.3 us, the first loads and scores 1.8 us, the output 2 us
-// (all SMs read and write in bursts); a step takes 2.2 us.
+// Measured: one sequence of 16,384 tokens, 16 heads over 4, causal: 1.04 ms,
+// 1,055 TFLOP/s (0.65 of the measured burst peak; clocks fall to 1.53 GHz
+// under it), about 3,450 cycles for a pair of steps where the tensor pipe alone
+// needs 2,048: each tile's chain of softmax, P V and Q K^T is what remains.
 //
 // TMEM: S_0 [0,128), S_1 [128,256), O_0 [256,256+d), O_1 [384,384+d).
-// Shared memory: Q_0, Q_1 (later the output tiles), kStages tiles of K or V.
+// Shared memory: Q_0, Q_1, kStages tiles of K or V, 4 KB of output per softmax warp.
 //
 // Rows of K and V behind the sequence belong to other sequences or to nobody:
 // their scores are replaced before use and their V rows are cleared in shared
@@ -69,7 +72,7 @@ constexpr int kTile = 128;  // query rows of a tile, keys of a step
 constexpr int kSms = 148;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 * tile
-constexpr int kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
+constexpr int kRegsLaunch = 168, kRegsLow = 56, kRegsHigh = 224;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kRegsLaunch * kThreads, "register split exceeds the launch");
 
 template <int D>
@@ -121,7 +124,7 @@ __device__ __forceinline__ int keys_below(const Prompt& p, const Span& s, int en
 // Row tiles (of R = 2^lr rows) of a sequence whose key steps number more than x.
 __device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int lr, int x) {
   const int T = (s.nq + (1 << lr) - 1) >> lr;
-  if (x < 0) return T;
+  if (x < 0 || T == 0) return T;
   if (!p.causal) return s.nk > kTile * x ? T : 0;
   if (s.nk <= kTile * x) return 0;  // the last tile sees all nk keys, none sees more
   // tile t (not the last) sees (t + 1) R + nk - nq keys
@@ -360,7 +363,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       };
       for (int r = 0; take(r, k); ++r) {
         const int n = __shfl_sync(0xffffffffu, k.n, 0), m0 = __shfl_sync(0xffffffffu, k.n0, 0),
-                  m1 = __shfl_sync(0xffffffffu, k.n1, 0);
+                  m1 = __shfl_sync(0xffffffffu, k.n1, 0), nk = __shfl_sync(0xffffffffu, k.seq.nk, 0);
         if (n == 0) continue;
         ok = wait(&full[st], par);
 #pragma unroll
@@ -384,8 +387,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           ok = wait(&full[sv], v_par);
           if (ok && j + 1 < n) ok = wait(&full[sk], k_par);
           if (!ok) break;
-          const int there = k.seq.nk - j * kTile;
-          if (there < kTile) {  // the last tile: clear the V rows behind the sequence
+          const int there = nk - j * kTile;
+          if (j == n - 1 && there < kTile) {  // the last tile: clear the V rows behind the sequence
             unsigned char* vst = smem + S::kRing + sv * S::kTileBytes;
             for (int e = there * 8 * S::kHalves + lane; e < kTile * 8 * S::kHalves; e += 32) {
               const int row = e / (8 * S::kHalves), ch = e % (8 * S::kHalves);
@@ -419,7 +422,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           advance(sk, k_par, 2);
         }
         if (!ok) break;
-        advance(st, par, 0);
         // 2 n tiles of the item, one of them taken above
         for (int left = 2 * n - 1; left > 0; left -= NS) advance(st, par, left < NS ? left : NS);
       }
@@ -670,7 +672,7 @@ cudaError_t run(const Prompt& p, const uint16_t* q, const uint16_t* k, const uin
   const int pair_heads = (p.H / p.H_kv) % 2 == 0 ? 1 : 0;
   const int R = pair_heads ? kTile : 2 * kTile;
   const long long tiles = static_cast<long long>(p.rows_q) / R + p.n_seq;  // at least the sequences' row tiles
-  const long long blocks = min(tiles * (pair_heads ? p.H / 2 : p.H), static_cast<long long>(kSms));
+  const long long most = tiles * (pair_heads ? p.H / 2 : p.H), blocks = min(most, static_cast<long long>(kSms));
   return launch_after(prompt_attn_kernel<D>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream, mq, mk, mv, p,
                       pair_heads, seq_q, seq_k, o, lse, status, serving_wait_limit());
 }

@@ -105,6 +105,22 @@ def test_prompt_many_sequences():
     check_prompt(q, k, v, sq, sq, True, o, lse)
 
 
+@pytest.mark.parametrize("H,H_kv,d,causal", [(16, 8, 128, True), (8, 8, 64, True), (16, 8, 64, False), (8, 8, 128, False)])
+def test_prompt_several_tiles_for_each_cta(H, H_kv, d, causal):
+    """Far more tiles than SMs, of unequal lengths, among them tiles without a visible key and sequences without
+    rows or keys: every CTA goes from one to the next."""
+    rng = np.random.default_rng(22)
+    nq = [int(x) for x in rng.integers(0, 60, 70)] + [300, 0, 140, 1]
+    nk = [int(x) for x in rng.integers(0, 60, 70)] + [310, 40, 10, 700]
+    sq, sk = offsets(nq), offsets(nk)
+    q, k, v = (bf16((int(a[-1]), h, d), rng).to(DEV) for a, h in ((sq, H), (sk, H_kv), (sk, H_kv)))
+    o, lse = run_prompt(q, k, v, sq, sk, causal)
+    check_prompt(q, k, v, sq, sk, causal, o, lse)
+    for _ in range(3):
+        again, lse2 = run_prompt(q, k, v, sq, sk, causal)
+        assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("scale", [0.5, 0.003])
 def test_prompt_scale_and_slices_of_one_projection(scale):
     rng = np.random.default_rng(6)
