@@ -422,10 +422,12 @@ class Workspace:
         self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
-        sda_workspace_init(self.ptr, self.nbytes, stream)
+        with torch.cuda.device(self.buf.device):
+            sda_workspace_init(self.ptr, self.nbytes, stream)
 
     def check(self, stream=None) -> None:
-        sda_read_status(self.ptr, self.nbytes, stream)
+        with torch.cuda.device(self.buf.device):
+            sda_read_status(self.ptr, self.nbytes, stream)
 
 
 def forward(p: SdaParams, q, k, v, p_q, p_k, g, ws: Optional[Workspace] = None, block_idx=None, stream=None):
