@@ -150,7 +150,9 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   int top = lane < p.n_seq ? mine.nk : 0;
   for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
   top = __reduce_max_sync(0xffffffffu, top);
-  out->valid = 0;
+  // one lane says that there is none, in order before the lane that finds it: the warp need not be converged
+  if (lane == 0) out->valid = 0;
+  __syncwarp();
   if (p.n_seq == 1) {  // one sequence: its tiles from the last
     const int T = (mine.nq + (1 << lr) - 1) >> lr;
     if (lane == 0 && i < T) *out = Item{1, mine.q0, mine.nq, mine.k0, mine.nk, T - 1 - i};

@@ -720,3 +720,21 @@ def test_serving_rows_apart():
     size = max(score_size(f64(q), O.cache_values(c.host, "k", c.table[b], t, block, h))
                for b, t in enumerate(lens) for h in range(H_kv))
     assert np.all(np.abs(f64(o) - want) <= attention_tolerance(want, spread, size, d, U_F16))
+
+
+@pytest.mark.parametrize("n", [[1], [100], [513], [64, 65], [3] * 40])
+def test_prompt_every_row_is_written_every_time(n):
+    """The search for a CTA's next tile says "none" and then "this one" in the same place; if the first store could
+    land last, a tile's rows would stay unwritten without a report. Many calls, each into fresh marks."""
+    rng = np.random.default_rng(30)
+    sq = offsets(n)
+    q, k, v = (bf16((int(sq[-1]), h, 64), rng).to(DEV) for h in (8, 2, 2))
+    p = sda.prompt_params(n_seq=len(n), rows_q=len(q), rows_k=len(q), H=8, H_kv=2, d=64)
+    ws, seq = sda.Workspace(p), dev(sq)
+    first, _ = run_prompt(q, k, v, sq, sq, True)
+    assert not torch.any(torch.isnan(first))
+    o = [torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(200)]
+    for x in o:
+        sda.sda_prompt_attn_fwd(p, q, k, v, seq, seq, x, None, ws.ptr, ws.nbytes)
+    ws.check()
+    assert all(torch.equal(x, first) for x in o)
