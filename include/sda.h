@@ -399,8 +399,9 @@ int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uin
  * max_new) is its token lens[b] - n_b + i and sees tokens 0 .. that one (append
  * its key first): o as in sda_prompt_attn_fwd, with the cache's values; a row
  * at a negative position sees nothing and gets zeros. Products of q (bf16,
- * brought to fp16 by an exact power of two per row) with the codes are exact,
- * P is rounded to fp16.
+ * brought to fp16 by an exact power of two per row) with the codes are exact.
+ * P times V's scale is rounded to fp16's 11 digits, term by term down to 2^-77
+ * of the row's largest such term; below 2^-88 of it a term counts as zero.
  * w_out (or NULL; needs weights = 1): w_out[slot] = w_in[slot] + the sum of the token's p over the
  * call's rows and the key head's query heads, for every token of the B
  * sequences; other slots of w_out stay as they are. w_in NULL counts as zeros;

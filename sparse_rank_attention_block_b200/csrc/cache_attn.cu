@@ -26,9 +26,21 @@
 // sequence can have more than kWholeTiles tiles, a CTA takes one whole unit.
 //
 // Scales differ from block to block. K's multiplies the scores. V's goes into
-// the exponent: with lv = log2 vs, the operand of P V is 2^(s + lv - mv) <= 1
-// with mv a running maximum of s + lv, so that fp16 holds it whatever the
-// scales are, while the sum takes 2^(s - m).
+// the exponent: with lv = log2 vs, the operand of P V is 2^(s + lv - mv) with
+// mv a running maximum of s + lv, while the sum takes 2^(s - m).
+//
+// That operand is fp16, the MMA's type with the most digits that E4M3 converts
+// to exactly. Taken 2^7 up it has full precision down to 2^-21 of the maximum.
+// Smaller terms decide an output whose largest term has a V near zero (a token
+// that draws attention and holds nothing, a block scaled for another channel),
+// so a tile that holds some takes P V in up to three passes over 2^28 each: the
+// precision is 2^-11 of every term down to 2^-77 of the maximum, and what is
+// below 2^-88 counts as zero. The passes cost such a tile its conversions and
+// MMAs again (131,072 tokens, 4 rows to a key head, every tile of this kind: 69
+// against 62.5 us); elsewhere they are a test of the least operand (16 sequences
+// of up to 4 new tokens 33.9 against 33.0 us, the other cases within the noise).
+// The first pass stands apart from the rare ones: in one loop with them it costs
+// the loads their head start (131,072 tokens 54.4 against 52.1 us).
 //
 // The order of channels and tokens inside an MMA is free (sums), so it is
 // chosen for the loads: a lane reads 16 contiguous bytes of a token at a time
@@ -74,6 +86,10 @@ constexpr int kLeast = 8;      // places of a stretch, at least
 constexpr int kLead = 8;
 constexpr int kWholeTiles = 16;
 constexpr int kMaxSeq = 65536;
+// fp16 operands of P: 2^kUp times their value, at most 2^15 (a reference may lag by 2^8), in full precision from
+// kLeastP on; two further passes, 2^kBand each, below that. The outputs then stay below 2^(15 + 9 + 24 + 56).
+constexpr int kUp = 7, kBand = 28;
+constexpr float kLeastP = 0x1p-14f;
 
 template <int D>
 struct Smem {
@@ -162,6 +178,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// The smaller of each pair of fp16 values, a NaN only where both are.
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ constexpr float exp2_of(int e) {  // -126 <= e <= 127
+  return __builtin_bit_cast(float, static_cast<uint32_t>(e + 127) << 23);
 }
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -532,68 +557,124 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             }
           }
       }
+      float p[NR][2][4];              // 2^(s + lv - mv + kUp)
       uint32_t pf[NR][2][2];          // P^T fragments of the two 16-token steps
+      bool small = false;             // some p below kLeastP (or a token that is not seen)
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
-        float p[2][4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float mr = finite_or_0(m[nr][u]), mvr = finite_or_0(mv[nr][u]);
           // 2^(s + lv - mv) = 2^(s - m) 2^(m + lv - mv)
-          const float fa = tc::ex2(fminf(mr + lv[0] - mvr, 127.f));
-          const float fb = HALVES ? tc::ex2(fminf(mr + lv[1] - mvr, 127.f)) : fa;
+          const float fa = tc::ex2(fminf(mr + lv[0] - mvr + kUp, 127.f));
+          const float fb = HALVES ? tc::ex2(fminf(mr + lv[1] - mvr + kUp, 127.f)) : fa;
           const float a0 = tc::ex2(s[nr][0][u] - mr), a1 = tc::ex2(s[nr][0][2 + u] - mr);
           const float b0 = tc::ex2(s[nr][1][u] - mr), b1 = tc::ex2(s[nr][1][2 + u] - mr);
           l[nr][u] += (a0 + a1) + (b0 + b1);
-          p[0][u] = a0 * fa;
-          p[0][2 + u] = a1 * fa;
-          p[1][u] = b0 * fb;
-          p[1][2 + u] = b1 * fb;
+          p[nr][0][u] = a0 * fa;
+          p[nr][0][2 + u] = a1 * fa;
+          p[nr][1][u] = b0 * fb;
+          p[nr][1][2 + u] = b1 * fb;
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          pf[nr][hf][0] = transpose8(pack_f16(p[hf][0], p[hf][1]));
-          pf[nr][hf][1] = transpose8(pack_f16(p[hf][2], p[hf][3]));
+          pf[nr][hf][0] = pack_f16(p[nr][hf][0], p[nr][hf][1]);
+          pf[nr][hf][1] = pack_f16(p[nr][hf][2], p[nr][hf][3]);
         }
+        const uint32_t least = min_f16x2(min_f16x2(pf[nr][0][0], pf[nr][0][1]), min_f16x2(pf[nr][1][0], pf[nr][1][1]));
+        small = small || (least & 0x7c00u) == 0u || (least & 0x7c000000u) == 0u;
       }
-      // O^T += V^T P^T: this lane's channels are those of group g4, two to an MMA; its tokens those of P
-      const bool clear = tok0 + kTok > seen || blk[0] < 0 || blk[1] < 0;  // V rows of no token of the sequence
+      // Terms that fp16 does not hold in full are left to further passes, each 2^kBand up (exactly, the output so far
+      // with them): a dominant token whose V is small leaves the output to them.
+      auto take = [&](float least) {  // operands: what is not below `least`; the rest stays in p, 2^kBand up
+        bool rest = false;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t w[4][D / 32];        // 4 tokens, d / 8 channels of the lane's group
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * hf + 8 * (e / 2) + (e % 2 ? t_hi : t_lo);
-          if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(row, spread(g4)));
-            w[e][0] = x.x;
-            w[e][1] = x.y;
-            w[e][2] = x.z;
-            w[e][3] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(row, g4 >> 1) + 8 * (g4 & 1));
-            w[e][0] = x.x;
-            w[e][1] = x.y;
+          for (int hf = 0; hf < 2; ++hf) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool now = !(p[nr][hf][e] < least);  // a NaN is taken, too
+              x[e] = now ? p[nr][hf][e] : 0.f;
+              p[nr][hf][e] = now ? 0.f : p[nr][hf][e] * exp2_of(kBand);
+              rest = rest || p[nr][hf][e] > 0.f;
+            }
+            pf[nr][hf][0] = pack_f16(x[0], x[1]);
+            pf[nr][hf][1] = pack_f16(x[2], x[3]);
           }
-          if (clear && (tok0 + row >= seen || blk[hf] < 0)) {
+        return __any_sync(0xffffffffu, rest) != 0;
+      };
+      const bool clear = tok0 + kTok > seen || blk[0] < 0 || blk[1] < 0;  // V rows of no token of the sequence
+      // O^T += V^T P^T: this lane's channels are those of group g4, two to an MMA; its tokens those of P
+      auto add_pv = [&] {
 #pragma unroll
-            for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            pf[nr][hf][0] = transpose8(pf[nr][hf][0]);
+            pf[nr][hf][1] = transpose8(pf[nr][hf][1]);
+          }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t w[4][D / 32];      // 4 tokens, d / 8 channels of the lane's group
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = 16 * hf + 8 * (e / 2) + (e % 2 ? t_hi : t_lo);
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + chunk_at<D>(row, spread(g4)));
+              w[e][0] = x.x;
+              w[e][1] = x.y;
+              w[e][2] = x.z;
+              w[e][3] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(vt + chunk_at<D>(row, g4 >> 1) + 8 * (g4 & 1));
+              w[e][0] = x.x;
+              w[e][1] = x.y;
+            }
+            if (clear && (tok0 + row >= seen || blk[hf] < 0)) {
+#pragma unroll
+              for (int f = 0; f < D / 32; ++f) w[e][f] = 0u;
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < D / 32; ++f) {
+            // channels 4 f .. 4 f + 3 of the group, tokens paired byte by byte
+            const uint32_t a01 = __byte_perm(w[0][f], w[1][f], 0x5140), a23 = __byte_perm(w[0][f], w[1][f], 0x7362);
+            const uint32_t b01 = __byte_perm(w[2][f], w[3][f], 0x5140), b23 = __byte_perm(w[2][f], w[3][f], 0x7362);
+            const uint32_t v0[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))};
+            const uint32_t v1[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
+                                    e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))};
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+              mma_f16(acc[nr][2 * f], v0, pf[nr][hf][0], pf[nr][hf][1]);
+              mma_f16(acc[nr][2 * f + 1], v1, pf[nr][hf][0], pf[nr][hf][1]);
+            }
           }
         }
+      };
+      auto scale_acc = [&](float by) {
 #pragma unroll
-        for (int f = 0; f < D / 32; ++f) {
-          // channels 4 f .. 4 f + 3 of the group, tokens paired byte by byte
-          const uint32_t a01 = __byte_perm(w[0][f], w[1][f], 0x5140), a23 = __byte_perm(w[0][f], w[1][f], 0x7362);
-          const uint32_t b01 = __byte_perm(w[2][f], w[3][f], 0x5140), b23 = __byte_perm(w[2][f], w[3][f], 0x7362);
-          const uint32_t v0[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a01)), e4m3x2_to_f16x2(static_cast<uint16_t>(a01 >> 16)),
-                                  e4m3x2_to_f16x2(static_cast<uint16_t>(b01)), e4m3x2_to_f16x2(static_cast<uint16_t>(b01 >> 16))};
-          const uint32_t v1[4] = {e4m3x2_to_f16x2(static_cast<uint16_t>(a23)), e4m3x2_to_f16x2(static_cast<uint16_t>(a23 >> 16)),
-                                  e4m3x2_to_f16x2(static_cast<uint16_t>(b23)), e4m3x2_to_f16x2(static_cast<uint16_t>(b23 >> 16))};
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
-            mma_f16(acc[nr][2 * f], v0, pf[nr][hf][0], pf[nr][hf][1]);
-            mma_f16(acc[nr][2 * f + 1], v1, pf[nr][hf][0], pf[nr][hf][1]);
-          }
+          for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[nr][j][e] *= by;
+      };
+      const bool bands = __any_sync(0xffffffffu, small) && take(kLeastP);
+      add_pv();
+      if (bands) {
+        scale_acc(exp2_of(kBand));
+        if (take(kLeastP)) {
+          add_pv();
+          scale_acc(exp2_of(kBand));
+          take(0.f);
+          add_pv();
+          scale_acc(exp2_of(-2 * kBand));
+        } else {
+          add_pv();
+          scale_acc(exp2_of(-kBand));
         }
       }
       __syncwarp();                   // every lane has read the stage
@@ -647,7 +728,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
         for (int u = 0; u < kWarps; ++u) {
           L = fmaf(st[u].y, tc::ex2(st[u].x - Mr), L);
-          f[u] = tc::ex2(st[u].z - MVr);
+          f[u] = tc::ex2(st[u].z - MVr) * exp2_of(-kUp);
         }
         const bool whole = tile == 0 && seg_all == sl.n_tiles;
         const int row = sl.nr.row0 + rr / g, head = hk * g + rr % g;

@@ -738,3 +738,58 @@ def test_prompt_every_row_is_written_every_time(n):
         sda.sda_prompt_attn_fwd(p, q, k, v, seq, seq, x, None, ws.ptr, ws.nbytes)
     ws.check()
     assert all(torch.equal(x, first) for x in o)
+
+
+WIDE_RANGES = [
+    # tokens, new rows, block, H, H_kv, d
+    ([300, 40], [1, 1], 32, 4, 2, 64),            # a CTA per unit
+    ([4097], [1], 64, 4, 1, 128),                 # split over many CTAs, a CTA joins a row
+    ([900, 30] * 12, [1] * 24, 64, 4, 2, 64),     # split, a warp joins a row
+    ([3000, 70], [2, 1], 16, 16, 1, 128),         # 16 rows to a tile, blocks of half a tile
+]
+
+
+def check_cache_attention(c, q):
+    o = c.attend(q)
+    c.ws.check()
+    want, spread, _ = O.cache_attention(f64(q), c.seq, c.lens, c.table, c.block, c.host)
+    size = max(score_size(f64(q), O.cache_values(c.host, "k", c.table[b], t, c.block, h))
+               for b, t in enumerate(c.lens) if t for h in range(c.H_kv))
+    tol = attention_tolerance(want, spread, size, c.d, U_F16)
+    err = np.abs(f64(o) - want)
+    assert np.all(err <= tol), f"worst error {np.max(err / tol):.2f} of the bound"
+    assert torch.equal(o, c.attend(q))
+
+
+@pytest.mark.parametrize("gap", [14, 16, 18, 20, 30, 45])
+@pytest.mark.parametrize("lens,new,block,H,H_kv,d", WIDE_RANGES)
+def test_cache_attention_dominant_token_that_holds_nothing(lens, new, block, H, H_kv, d, gap):
+    """Token 0 `gap` nats above the rest with a V of zero: the output is that of all the others, whose weights are
+    far below fp16's range under the row's largest. The bound counts a rounding of 2^-11 for each of them."""
+    rng = np.random.default_rng(gap)
+    c = Cache(rng, lens, block, H, H_kv, d, new)
+    c.host["k_scale"][:] = 2.0 ** -7
+    top = 2.0 if gap > 28 else 1.0                # q: the same number everywhere, so that a constant K gives its score
+    for b in range(len(lens)):
+        c.host["k_codes"][c.table[b, 0], :, 0] = O.encode_e4m3(np.float32(gap * 2.0 ** 7 / (top * d ** 0.5)))
+        c.host["v_codes"][c.table[b, 0], :, 0] = 0
+    c.pool = {n: dev(x) for n, x in c.host.items()}
+    c.free_slots_hold_nan()
+    check_cache_attention(c, torch.full((int(c.seq[-1]), H, d), top, dtype=torch.bfloat16, device=DEV))
+
+
+@pytest.mark.parametrize("binades", [20, 40, 60])
+@pytest.mark.parametrize("lens,new,block,H,H_kv,d", WIDE_RANGES)
+def test_cache_attention_block_scaled_for_another_channel(lens, new, block, H, H_kv, d, binades):
+    """A block whose V is scaled far above the others' for one channel and zero elsewhere: the other channels' output
+    comes from the other blocks alone."""
+    rng = np.random.default_rng(binades)
+    c = Cache(rng, lens, block, H, H_kv, d, new)
+    for b in range(len(lens)):
+        blk = c.table[b, (lens[b] - 1) // block // 2]
+        c.host["v_scale"][blk] = 2.0 ** (binades - 7)
+        c.host["v_codes"][blk] = 0
+        c.host["v_codes"][blk, :, ::3, 5] = 0x7E  # 448 in one channel of every third token
+    c.pool = {n: dev(x) for n, x in c.host.items()}
+    c.free_slots_hold_nan()
+    check_cache_attention(c, bf16((int(c.seq[-1]), H, d), rng).to(DEV))
