@@ -90,6 +90,8 @@ constexpr int kMaxSeq = 65536;
 // kLeastP on; two further passes, 2^kBand each, below that. The outputs then stay below 2^(15 + 9 + 24 + 56).
 constexpr int kUp = 7, kBand = 28;
 constexpr float kLeastP = 0x1p-14f;
+// 2^(s - m) is zero below 2^-126: no loss where P is at most 2^kFarUp times it, and the least that counts 2^-81.
+constexpr float kFarUp = 40.f;
 
 template <int D>
 struct Smem {
@@ -560,14 +562,16 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       float p[NR][2][4];              // 2^(s + lv - mv + kUp)
       uint32_t pf[NR][2][2];          // P^T fragments of the two 16-token steps
       bool small = false;             // some p below kLeastP (or a token that is not seen)
+      bool far = false;               // some p too far above its 2^(s - m)
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const float mr = finite_or_0(m[nr][u]), mvr = finite_or_0(mv[nr][u]);
           // 2^(s + lv - mv) = 2^(s - m) 2^(m + lv - mv)
-          const float fa = tc::ex2(fminf(mr + lv[0] - mvr + kUp, 127.f));
-          const float fb = HALVES ? tc::ex2(fminf(mr + lv[1] - mvr + kUp, 127.f)) : fa;
+          const float up_a = mr + lv[0] - mvr + kUp, up_b = mr + lv[HALVES ? 1 : 0] - mvr + kUp;
+          const float fa = tc::ex2(up_a), fb = HALVES ? tc::ex2(up_b) : fa;
+          far = far || fmaxf(up_a, up_b) > kFarUp;
           const float a0 = tc::ex2(s[nr][0][u] - mr), a1 = tc::ex2(s[nr][0][2 + u] - mr);
           const float b0 = tc::ex2(s[nr][1][u] - mr), b1 = tc::ex2(s[nr][1][2 + u] - mr);
           l[nr][u] += (a0 + a1) + (b0 + b1);
@@ -582,7 +586,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           pf[nr][hf][1] = pack_f16(p[nr][hf][2], p[nr][hf][3]);
         }
         const uint32_t least = min_f16x2(min_f16x2(pf[nr][0][0], pf[nr][0][1]), min_f16x2(pf[nr][1][0], pf[nr][1][1]));
-        small = small || (least & 0x7c00u) == 0u || (least & 0x7c000000u) == 0u;
+        small = small || far || (least & 0x7c00u) == 0u || (least & 0x7c000000u) == 0u;
       }
       // Terms that fp16 does not hold in full are left to further passes, each 2^kBand up (exactly, the output so far
       // with them): a dominant token whose V is small leaves the output to them.
@@ -662,7 +666,19 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[nr][j][e] *= by;
       };
-      const bool bands = __any_sync(0xffffffffu, small) && take(kLeastP);
+      bool bands = false;
+      if (__any_sync(0xffffffffu, small)) {
+        if (__any_sync(0xffffffffu, far)) {  // in one step: 2^(s - m) would be zero where its V's scale makes up for it
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                p[nr][hf][e] = tc::ex2(s[nr][hf][e] + (lv[hf] - finite_or_0(mv[nr][e % 2]) + kUp));
+        }
+        bands = take(kLeastP);
+      }
       add_pv();
       if (bands) {
         scale_acc(exp2_of(kBand));

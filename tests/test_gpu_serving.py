@@ -793,3 +793,28 @@ def test_cache_attention_block_scaled_for_another_channel(lens, new, block, H, H
     c.pool = {n: dev(x) for n, x in c.host.items()}
     c.free_slots_hold_nan()
     check_cache_attention(c, bf16((int(c.seq[-1]), H, d), rng).to(DEV))
+
+
+@pytest.mark.parametrize("code", [176.0, 192.0])
+@pytest.mark.parametrize("lens,new,block,H,H_kv,d", WIDE_RANGES)
+def test_cache_attention_scale_makes_up_for_a_tiny_weight(lens, new, block, H, H_kv, d, code):
+    """A block whose probabilities are below 2^-126 of the row's largest, with V's scale as far above the others':
+    it takes its share of the output."""
+    rng = np.random.default_rng(int(code))
+    c = Cache(rng, lens, block, H, H_kv, d, new)
+    c.host["k_scale"][:] = 2.0 ** -7
+    c.host["v_scale"][:] = 2.0 ** -20
+    for b in range(len(lens)):
+        blk = c.table[b, (lens[b] - 1) // block // 2]
+        c.host["k_codes"][blk], c.host["k_scale"][blk] = O.encode_e4m3(np.float32(-code)), 2.0 ** -5
+        nats = 2 * code * 2.0 ** -5 * d ** 0.5    # under q = 2 everywhere
+        while nats > 96:                          # keep the scale within fp32: d = 128
+            c.host["k_scale"][blk] /= 2
+            nats /= 2
+        if nats < 80:
+            c.host["k_codes"][blk] = O.encode_e4m3(np.float32(-code * 88 / nats))
+            nats = 88
+        c.host["v_scale"][blk] = 2.0 ** (round(nats / np.log(2)) - 20)
+    c.pool = {n: dev(x) for n, x in c.host.items()}
+    c.free_slots_hold_nan()
+    check_cache_attention(c, torch.full((int(c.seq[-1]), H, d), 2.0, dtype=torch.bfloat16, device=DEV))
