@@ -11,6 +11,7 @@ There is no CPU fallback: if libsda.so is missing the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -269,15 +270,15 @@ def _refuse(where: str, what: str, code: int = -3):
     raise SdaError(code, where, what)
 
 
-def _dense(where, dev, t, name, dtype, numel):
-    """Pointer of a dense tensor of this type and size on device number `dev`.
+def _dense(where, dev, t, name, dtype, shape):
+    """Pointer of a dense tensor of this type and shape (or flat, of as many elements) on device number `dev`.
 
-    These checks run on every call of a decoding step, so each is one cheap
-    property of the tensor; the shape itself does not matter to the library."""
+    The order of the dimensions is part of what a call means: the same bytes in another order are refused. These
+    checks run on every call of a decoding step, so each is one cheap property of the tensor."""
     if t is None or type(t) is int:
         return t
-    if t.dtype is not dtype or t.nbytes != numel * dtype.itemsize or not t.is_contiguous():
-        _refuse(where, f"{name} must be a dense {dtype} tensor of {numel} elements "
+    if t.dtype is not dtype or (t.shape != shape and t.shape != (math.prod(shape),)) or not t.is_contiguous():
+        _refuse(where, f"{name} must be a dense {dtype} tensor of shape {shape} "
                        f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()})")
     if t.get_device() != dev:
         _refuse(where, f"{name} is on {t.device}, not on cuda:{dev}", -8)
@@ -339,17 +340,17 @@ def sda_prompt_attn_fwd(p: SdaPromptParams, q, k, v, seq_q, seq_k, o, lse, ws, n
     _call(f, dev, p, (_rows(f, dev, q, "q", p.rows_q, p.H, p.d, p.ld_q),
                       _rows(f, dev, k, "k", p.rows_k, p.H_kv, p.d, p.ld_k),
                       _rows(f, dev, v, "v", p.rows_k, p.H_kv, p.d, p.ld_v),
-                      _dense(f, dev, seq_q, "seq_q", _I32, p.n_seq + 1),
-                      _dense(f, dev, seq_k, "seq_k", _I32, p.n_seq + 1),
+                      _dense(f, dev, seq_q, "seq_q", _I32, (p.n_seq + 1,)),
+                      _dense(f, dev, seq_k, "seq_k", _I32, (p.n_seq + 1,)),
                       _rows(f, dev, o, "o", p.rows_q, p.H, p.d, p.ld_o),
-                      _dense(f, dev, lse, "lse", _F32, p.rows_q * p.H)), ws, nbytes, stream)
+                      _dense(f, dev, lse, "lse", _F32, (p.rows_q, p.H))), ws, nbytes, stream)
 
 
 def _pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale):
-    scales = p.n_blocks * p.H_kv
-    codes = scales * p.block * p.d
-    return (_dense(f, dev, lens, "lens", _I32, p.B),
-            _dense(f, dev, block_table, "block_table", _I32, p.B * p.max_blocks),
+    scales = (p.n_blocks, p.H_kv)
+    codes = (*scales, p.block, p.d)
+    return (_dense(f, dev, lens, "lens", _I32, (p.B,)),
+            _dense(f, dev, block_table, "block_table", _I32, (p.B, p.max_blocks)),
             _dense(f, dev, k_codes, "k_codes", _U8, codes), _dense(f, dev, v_codes, "v_codes", _U8, codes),
             _dense(f, dev, k_scale, "k_scale", _F32, scales), _dense(f, dev, v_scale, "v_scale", _F32, scales))
 
@@ -360,18 +361,18 @@ def sda_cache_append(p: SdaCacheParams, k, v, seq, lens, block_table, k_codes, v
     dev = _device_of(f, k, v, k_codes)
     _call(f, dev, p, (_rows(f, dev, k, "k", p.rows, p.H_kv, p.d, p.ld_k),
                       _rows(f, dev, v, "v", p.rows, p.H_kv, p.d, p.ld_v),
-                      _dense(f, dev, seq, "seq", _I32, p.B + 1),
+                      _dense(f, dev, seq, "seq", _I32, (p.B + 1,)),
                       *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
-                      _dense(f, dev, w, "w", _F32, p.n_blocks * p.H_kv * p.block)), ws, nbytes, stream)
+                      _dense(f, dev, w, "w", _F32, (p.n_blocks, p.H_kv, p.block))), ws, nbytes, stream)
 
 
 def sda_cache_attn_fwd(p: SdaCacheParams, q, seq, lens, block_table, k_codes, v_codes, k_scale, v_scale, w_in, w_out, o,
                        ws, nbytes, stream=None) -> None:
     f = "sda_cache_attn_fwd"
     dev = _device_of(f, q, o, k_codes)
-    slots = p.n_blocks * p.H_kv * p.block
+    slots = (p.n_blocks, p.H_kv, p.block)
     _call(f, dev, p, (_rows(f, dev, q, "q", p.rows, p.H, p.d, p.ld_q),
-                      _dense(f, dev, seq, "seq", _I32, p.B + 1),
+                      _dense(f, dev, seq, "seq", _I32, (p.B + 1,)),
                       *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
                       _dense(f, dev, w_in, "w_in", _F32, slots), _dense(f, dev, w_out, "w_out", _F32, slots),
                       _rows(f, dev, o, "o", p.rows, p.H, p.d, p.ld_o)), ws, nbytes, stream)
@@ -382,10 +383,10 @@ def sda_cache_evict(p: SdaCacheParams, lens, block_table, k_codes, v_codes, k_sc
     f = "sda_cache_evict"
     dev = _device_of(f, k_codes, v_codes, w)
     _call(f, dev, p, (*_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
-                      _dense(f, dev, w, "w", _F32, p.n_blocks * p.H_kv * p.block),
-                      _dense(f, dev, dst_table, "dst_table", _I32, p.B * -(-p.keep // p.block)),
-                      _dense(f, dev, kept, "kept", _I32, p.B * p.H_kv * p.keep),
-                      _dense(f, dev, dst_lens, "dst_lens", _I32, p.B)), ws, nbytes, stream)
+                      _dense(f, dev, w, "w", _F32, (p.n_blocks, p.H_kv, p.block)),
+                      _dense(f, dev, dst_table, "dst_table", _I32, (p.B, -(-p.keep // p.block))),
+                      _dense(f, dev, kept, "kept", _I32, (p.B, p.H_kv, p.keep)),
+                      _dense(f, dev, dst_lens, "dst_lens", _I32, (p.B,))), ws, nbytes, stream)
 
 
 def sda_forward_host_buffer_size(p: SdaParams) -> int:

@@ -148,3 +148,38 @@ def test_cache_wrappers_refuse_tensors(L):
                 with pytest.raises(sda.SdaError) as e:
                     fn(c, *args[:i], wrong, *args[i + 1:], 256, 1 << 30, stream=0)
                 assert e.value.code == -3, (fn.__name__, i)
+
+
+def _cache_calls():
+    """Each cache call's wrapper with host tensors of the right types and shapes, for cache(weights=True)."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    codes, scale, w = torch.zeros(8, 2, 16, 64, dtype=torch.uint8), torch.zeros(8, 2), torch.zeros(8, 2, 16)
+    pool = [i32(2), i32(2, 4), codes, codes.clone(), scale, scale.clone()]
+    return [(sda.sda_cache_append, [bf(2, 2, 64), bf(2, 2, 64), i32(3), *pool, w]),
+            (sda.sda_cache_attn_fwd, [bf(2, 4, 64), i32(3), *pool, w, w, bf(2, 4, 64)]),
+            (sda.sda_cache_evict, [*pool, w, i32(2, 1), i32(2, 2, 16), i32(2)])]
+
+
+def test_wrappers_refuse_the_same_bytes_in_another_order(L):
+    """Codes as [n_blocks, block, H_kv, d], scales by head, a table by column, lse by head: as many bytes, other
+    meaning. A flat tensor says nothing about the order and is taken."""
+    t = _tensors()
+    t["lse"] = torch.zeros(4, 10)
+    with pytest.raises(sda.SdaError) as e:
+        sda.sda_prompt_attn_fwd(prompt(), *t.values(), 256, 256, stream=0)
+    assert e.value.code == -3 and "lse" in str(e.value)
+    for fn, args in _cache_calls():
+        for i, a in enumerate(args):
+            if a.dim() < 2 or a.dtype is torch.bfloat16 or a.shape[0] == a.shape[1]:
+                continue                                   # equal extents: nothing tells the orders apart
+            with pytest.raises(sda.SdaError) as e:
+                fn(cache(weights=True), *args[:i], a.transpose(0, 1).contiguous(), *args[i + 1:], 256, 1 << 30, stream=0)
+            assert e.value.code == -3, (fn.__name__, i)
+            with pytest.raises(sda.SdaError) as e:         # the layout passes, the place does not
+                fn(cache(weights=True), *args[:i], a.flatten(), *args[i + 1:], 256, 1 << 30, stream=0)
+            assert e.value.code == -8, (fn.__name__, i)
+        swapped = [a.transpose(1, 2).contiguous() if a.dim() == 4 else a for a in args]
+        with pytest.raises(sda.SdaError) as e:
+            fn(cache(weights=True), *swapped, 256, 1 << 30, stream=0)
+        assert e.value.code == -3 and "k_codes" in str(e.value)
