@@ -263,7 +263,7 @@ def sda_forward_profiled(p, q, k, v, p_q, p_k, g, o, block_idx_out, ws, nbytes, 
 # serving operators: tensors are checked against the parameters (raw pointers are taken as they are)
 # ---------------------------------------------------------------------------
 
-_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+_BF16, _I32, _F32, _U8, _E4M3 = torch.bfloat16, torch.int32, torch.float32, torch.uint8, torch.float8_e4m3fn
 
 
 def _refuse(where: str, what: str, code: int = -3):
@@ -273,11 +273,13 @@ def _refuse(where: str, what: str, code: int = -3):
 def _dense(where, dev, t, name, dtype, shape):
     """Pointer of a dense tensor of this type and shape (or flat, of as many elements) on device number `dev`.
 
-    The order of the dimensions is part of what a call means: the same bytes in another order are refused. These
-    checks run on every call of a decoding step, so each is one cheap property of the tensor."""
+    The order of the dimensions is part of what a call means: the same bytes in another order are refused. E4M3 codes
+    may be bytes or torch's own type. These checks run on every call of a decoding step, so each is one cheap property
+    of the tensor."""
     if t is None or type(t) is int:
         return t
-    if t.dtype is not dtype or (t.shape != shape and t.shape != (math.prod(shape),)) or not t.is_contiguous():
+    if (t.dtype is not dtype and not (dtype is _U8 and t.dtype is _E4M3)) or \
+            (t.shape != shape and t.shape != (math.prod(shape),)) or not t.is_contiguous():
         _refuse(where, f"{name} must be a dense {dtype} tensor of shape {shape} "
                        f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()})")
     if t.get_device() != dev:
@@ -337,56 +339,58 @@ def sda_cache_workspace_size(p: SdaCacheParams) -> int:
 def sda_prompt_attn_fwd(p: SdaPromptParams, q, k, v, seq_q, seq_k, o, lse, ws, nbytes, stream=None) -> None:
     f = "sda_prompt_attn_fwd"
     dev = _device_of(f, q, k, v, o)
-    _call(f, dev, p, (_rows(f, dev, q, "q", p.rows_q, p.H, p.d, p.ld_q),
-                      _rows(f, dev, k, "k", p.rows_k, p.H_kv, p.d, p.ld_k),
-                      _rows(f, dev, v, "v", p.rows_k, p.H_kv, p.d, p.ld_v),
-                      _dense(f, dev, seq_q, "seq_q", _I32, (p.n_seq + 1,)),
-                      _dense(f, dev, seq_k, "seq_k", _I32, (p.n_seq + 1,)),
-                      _rows(f, dev, o, "o", p.rows_q, p.H, p.d, p.ld_o),
-                      _dense(f, dev, lse, "lse", _F32, (p.rows_q, p.H))), ws, nbytes, stream)
+    n, rows_q, rows_k, H, H_kv, d = p.n_seq, p.rows_q, p.rows_k, p.H, p.H_kv, p.d
+    _call(f, dev, p, (_rows(f, dev, q, "q", rows_q, H, d, p.ld_q), _rows(f, dev, k, "k", rows_k, H_kv, d, p.ld_k),
+                      _rows(f, dev, v, "v", rows_k, H_kv, d, p.ld_v),
+                      _dense(f, dev, seq_q, "seq_q", _I32, (n + 1,)), _dense(f, dev, seq_k, "seq_k", _I32, (n + 1,)),
+                      _rows(f, dev, o, "o", rows_q, H, d, p.ld_o), _dense(f, dev, lse, "lse", _F32, (rows_q, H))),
+          ws, nbytes, stream)
 
 
 def _pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale):
-    scales = (p.n_blocks, p.H_kv)
-    codes = (*scales, p.block, p.d)
-    return (_dense(f, dev, lens, "lens", _I32, (p.B,)),
-            _dense(f, dev, block_table, "block_table", _I32, (p.B, p.max_blocks)),
+    B, n, H_kv = p.B, p.n_blocks, p.H_kv                     # a field's read costs as much as a check
+    scales, codes = (n, H_kv), (n, H_kv, p.block, p.d)
+    return (_dense(f, dev, lens, "lens", _I32, (B,)), _dense(f, dev, block_table, "block_table", _I32, (B, p.max_blocks)),
             _dense(f, dev, k_codes, "k_codes", _U8, codes), _dense(f, dev, v_codes, "v_codes", _U8, codes),
             _dense(f, dev, k_scale, "k_scale", _F32, scales), _dense(f, dev, v_scale, "v_scale", _F32, scales))
+
+
+def _slots(p):
+    return p.n_blocks, p.H_kv, p.block
 
 
 def sda_cache_append(p: SdaCacheParams, k, v, seq, lens, block_table, k_codes, v_codes, k_scale, v_scale, w, ws, nbytes,
                      stream=None) -> None:
     f = "sda_cache_append"
     dev = _device_of(f, k, v, k_codes)
-    _call(f, dev, p, (_rows(f, dev, k, "k", p.rows, p.H_kv, p.d, p.ld_k),
-                      _rows(f, dev, v, "v", p.rows, p.H_kv, p.d, p.ld_v),
+    rows, H_kv, d = p.rows, p.H_kv, p.d
+    _call(f, dev, p, (_rows(f, dev, k, "k", rows, H_kv, d, p.ld_k), _rows(f, dev, v, "v", rows, H_kv, d, p.ld_v),
                       _dense(f, dev, seq, "seq", _I32, (p.B + 1,)),
                       *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
-                      _dense(f, dev, w, "w", _F32, (p.n_blocks, p.H_kv, p.block))), ws, nbytes, stream)
+                      _dense(f, dev, w, "w", _F32, _slots(p))), ws, nbytes, stream)
 
 
 def sda_cache_attn_fwd(p: SdaCacheParams, q, seq, lens, block_table, k_codes, v_codes, k_scale, v_scale, w_in, w_out, o,
                        ws, nbytes, stream=None) -> None:
     f = "sda_cache_attn_fwd"
     dev = _device_of(f, q, o, k_codes)
-    slots = (p.n_blocks, p.H_kv, p.block)
-    _call(f, dev, p, (_rows(f, dev, q, "q", p.rows, p.H, p.d, p.ld_q),
-                      _dense(f, dev, seq, "seq", _I32, (p.B + 1,)),
+    rows, H, d = p.rows, p.H, p.d
+    _call(f, dev, p, (_rows(f, dev, q, "q", rows, H, d, p.ld_q), _dense(f, dev, seq, "seq", _I32, (p.B + 1,)),
                       *_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
-                      _dense(f, dev, w_in, "w_in", _F32, slots), _dense(f, dev, w_out, "w_out", _F32, slots),
-                      _rows(f, dev, o, "o", p.rows, p.H, p.d, p.ld_o)), ws, nbytes, stream)
+                      *((None, None) if w_in is w_out is None else
+                        (_dense(f, dev, w_in, "w_in", _F32, _slots(p)), _dense(f, dev, w_out, "w_out", _F32, _slots(p)))),
+                      _rows(f, dev, o, "o", rows, H, d, p.ld_o)), ws, nbytes, stream)
 
 
 def sda_cache_evict(p: SdaCacheParams, lens, block_table, k_codes, v_codes, k_scale, v_scale, w, dst_table, kept,
                     dst_lens, ws, nbytes, stream=None) -> None:
     f = "sda_cache_evict"
     dev = _device_of(f, k_codes, v_codes, w)
+    B, keep = p.B, p.keep
     _call(f, dev, p, (*_pool(f, dev, p, lens, block_table, k_codes, v_codes, k_scale, v_scale),
-                      _dense(f, dev, w, "w", _F32, (p.n_blocks, p.H_kv, p.block)),
-                      _dense(f, dev, dst_table, "dst_table", _I32, (p.B, -(-p.keep // p.block))),
-                      _dense(f, dev, kept, "kept", _I32, (p.B, p.H_kv, p.keep)),
-                      _dense(f, dev, dst_lens, "dst_lens", _I32, (p.B,))), ws, nbytes, stream)
+                      _dense(f, dev, w, "w", _F32, _slots(p)), _dense(f, dev, dst_table, "dst_table", _I32, (B, -(-keep // p.block))),
+                      _dense(f, dev, kept, "kept", _I32, (B, p.H_kv, keep)),
+                      _dense(f, dev, dst_lens, "dst_lens", _I32, (B,))), ws, nbytes, stream)
 
 
 def sda_forward_host_buffer_size(p: SdaParams) -> int:

@@ -818,3 +818,19 @@ def test_cache_attention_scale_makes_up_for_a_tiny_weight(lens, new, block, H, H
     c.pool = {n: dev(x) for n, x in c.host.items()}
     c.free_slots_hold_nan()
     check_cache_attention(c, torch.full((int(c.seq[-1]), H, d), 2.0, dtype=torch.bfloat16, device=DEV))
+
+
+def test_cache_codes_in_torchs_own_type():
+    """torch.float8_e4m3fn codes are the same bytes."""
+    rng = np.random.default_rng(31)
+    c = Cache(rng, [50, 33], 16, 4, 2, 64, [2, 1])
+    q, k, v = (bf16((3, h, 64), rng).to(DEV) for h in (4, 2, 2))
+    O.append(f64(k), f64(v), c.seq, c.lens, c.table, 16, c.host)
+    for n in ("k_codes", "v_codes"):
+        c.pool[n] = c.pool[n].view(torch.float8_e4m3fn)
+    c.append(k, v, w=False)
+    o = c.attend(q)
+    for n in ("k_codes", "v_codes"):
+        c.pool[n] = c.pool[n].view(torch.uint8)
+    c.check_pool()
+    assert torch.equal(o, c.attend(q))

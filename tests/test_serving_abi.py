@@ -183,3 +183,12 @@ def test_wrappers_refuse_the_same_bytes_in_another_order(L):
         with pytest.raises(sda.SdaError) as e:
             fn(cache(weights=True), *swapped, 256, 1 << 30, stream=0)
         assert e.value.code == -3 and "k_codes" in str(e.value)
+
+
+def test_wrappers_take_codes_in_torchs_own_type(L):
+    for fn, args in _cache_calls():
+        for kind, code in ((torch.float8_e4m3fn, -8), (torch.float8_e5m2, -3), (torch.int8, -3)):  # -8: the layout passes
+            typed = [a.view(kind) if a.dtype is torch.uint8 else a for a in args]
+            with pytest.raises(sda.SdaError) as e:
+                fn(cache(weights=True), *typed, 256, 1 << 30, stream=0)
+            assert e.value.code == code, (fn.__name__, kind)
