@@ -122,7 +122,9 @@ int32_t sda_workspace_init(void* ws, size_t ws_bytes, void* stream);
  * Returns SDA_OK; SDA_ERR_TIMEOUT if a kernel gave up a bounded wait since the
  * last read; SDA_ERR_SHAPE if the sparse attention met a block index outside
  * [0, N_kblk) (with a causal window: outside the [0, n_c) candidates of the
- * query block's chunk) and skipped it. The affected outputs are then undefined. */
+ * query block's chunk) and skipped it, or a serving call an offset, a length, a
+ * block number or a scale outside its range. The affected outputs are then
+ * undefined. */
 int32_t sda_read_status(void* ws, size_t ws_bytes, void* stream);
 
 /* Block selector (robotworld summary, section 2.1: A_M keeps a 1 - s
@@ -356,7 +358,9 @@ int32_t sda_prompt_attn_fwd(const sda_prompt_params* p, const uint16_t* q, const
 
 /* The cache: a pool of n_blocks blocks of `block` tokens. k_codes, v_codes:
  * [n_blocks, H_kv, block, d] E4M3 bytes; k_scale, v_scale: [n_blocks, H_kv]
- * fp32, a value being its code times the scale of its block and head; w (where
+ * fp32, a value being its code times the scale of its block and head (finite
+ * and not negative: other scales that a call meets are reported as
+ * SDA_ERR_SHAPE, and what it makes of their sequence is undefined); w (where
  * weights are collected): [n_blocks, H_kv, block] fp32. block_table: [B,
  * max_blocks] int32, the pool's block that holds tokens t * block .. of a
  * sequence; entries behind the sequence's last block are not read. lens: [B]

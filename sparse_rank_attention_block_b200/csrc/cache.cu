@@ -104,7 +104,10 @@ __global__ void cache_append_kernel(Cache c, int touched, int units, const uint1
     for (int g = 0; g < warps; ++g) m = max(m, tops[g]);
     const float want = wanted_scale(m);
     const float after = slot0 > 0 ? fmaxf(before, want) : want;
-    if (threadIdx.x == 0) *scale = after;
+    if (threadIdx.x == 0) {
+      *scale = after;
+      if (!is_scale(before)) report_status(status, kStatusBadIndex);
+    }
     if (slot0 > 0 && before != after) {
       const Rescale again(before / after);
       for (int row = row0; row < slot0; row += step) {
@@ -365,7 +368,7 @@ __global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uin
     scale[1][r] = bb;
   }
   __syncthreads();
-  // scales are positive: their bits order like their values
+  // scales are not negative: their bits order like their values
   uint32_t k_top = 0u, v_top = 0u;
   for (int r = t % 32; r < c.block; r += 32) {
     k_top = max(k_top, __float_as_uint(scale[0][r]));
@@ -376,6 +379,7 @@ __global__ void cache_move_kernel(Cache c, const int32_t* __restrict__ lens, uin
   if (t == 0) {
     k_scale[dst_head] = ks;
     v_scale[dst_head] = vs;
+    if (!(is_scale(ks) && is_scale(vs))) report_status(status, kStatusBadIndex);  // the largest bits: all are or it is not
   }
   for (int r = t; r < c.block; r += blockDim.x) {
     ratio[0][r] = ks > 0.f ? scale[0][r] / ks : 1.f;

@@ -465,6 +465,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
       ok = tc::wait_warp(&full[st], ((done + i) / kStages) & 1, abort_flag, a.wait_ns);
       if (!ok) break;                 // the load stays counted as issued
+      if (i % 16 == 0 && !(is_scale(now.ks) && is_scale(now.vs))) report_status(a.status, kStatusBadIndex);
       const unsigned char* kt = ring + st * S::kStage;
       const unsigned char* vt = kt + S::kHalf;
 

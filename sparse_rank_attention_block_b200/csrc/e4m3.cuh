@@ -34,6 +34,9 @@ __device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
   return r;
 }
 
+// What a block's scale may be: finite and not negative (by its bits, so that of several the largest bits tell).
+__device__ __forceinline__ bool is_scale(float x) { return __float_as_uint(x) < 0x7f800000u; }
+
 // Four codes under a scale, written anew under another: ratio = old / new <= 1.
 // By a power of two fp16 takes the products exactly where they decide: a code
 // has 4 significant bits, so what is not below 2^-10 (which rounds to zero) has

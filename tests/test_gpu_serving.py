@@ -834,3 +834,63 @@ def test_cache_codes_in_torchs_own_type():
         c.pool[n] = c.pool[n].view(torch.uint8)
     c.check_pool()
     assert torch.equal(o, c.attend(q))
+
+
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("value", [-1.0, float("nan"), float("inf"), 0.0])
+def test_cache_scales_outside_their_range_are_reported(which, value):
+    """Negative, NaN and infinite scales of a sequence's blocks; zero is a scale, and blocks of nobody do not count."""
+    rng = np.random.default_rng(32)
+    for at, seen in ((0, True), (1, True), (None, False)):       # the first block, the last one, one of nobody
+        c = Cache(rng, [60, 40], 32, 2, 1, 64, [1, 1], keep=32, recent=2, extra=4)
+        free = [b for b in range(c.n_blocks) if b not in c.table]
+        blk = free.pop() if at is None else c.table[0, at]
+        c.host[which][blk] = value
+        c.pool[which] = dev(c.host[which])
+        q, x = bf16((2, 2, 64), rng).to(DEV), bf16((2, 1, 64), rng).to(DEV)
+        dst = np.array([[free.pop()], [free.pop()]], np.int32)
+        kept, n = torch.empty((2, 1, 32), dtype=torch.int32, device=DEV), torch.empty(2, dtype=torch.int32, device=DEV)
+        c.w[:] = 0
+        c.w[c.table[0, 0]] = 1                                   # tokens of the first block stay, and the newest two
+        c.w_dev = dev(c.w)
+        calls = [lambda: c.attend(q),
+                 lambda: sda.sda_cache_evict(c.p, *c.args(), c.w_dev, dev(dst), kept, n, c.ws.ptr, c.ws.nbytes),
+                 lambda: c.append(x, x, w=False)]
+        for i, call in enumerate(calls):
+            call()
+            # an append touches the last block alone
+            if value == 0.0 or not seen or (i == 2 and at == 0):
+                c.ws.check()
+                continue
+            with pytest.raises(sda.SdaError) as e:
+                c.ws.check()
+            assert e.value.code == -3, (i, at)
+            c.ws.check()
+
+
+def test_cache_scale_of_zero():
+    """A block whose scale is zero holds zeros: under attention, under an append that goes on in it, and under
+    eviction beside others."""
+    rng = np.random.default_rng(33)
+    c = Cache(rng, [60, 40], 32, 2, 1, 64, [1, 1], keep=32, recent=16, extra=4)
+    for n in ("k_scale", "v_scale"):
+        c.host[n][c.table[0, 1]] = 0.0
+    c.host["v_scale"][c.table[1, :2]] = 0.0                       # all of a sequence's V
+    c.pool = {n: dev(x) for n, x in c.host.items()}
+    q, k, v = (bf16((2, h, 64), rng).to(DEV) for h in (2, 1, 1))
+    check_cache_attention(c, q)
+    assert torch.all(c.attend(q)[1] == 0)
+    free = [b for b in range(c.n_blocks) if b not in c.table]
+    dst = np.array([[free[0]], [-1]], np.int32)                   # one sequence: a block of zeros only has no largest scale
+    lens, c.lens = c.lens, [60, 0]
+    kept, n = torch.empty((2, 1, 32), dtype=torch.int32, device=DEV), torch.empty(2, dtype=torch.int32, device=DEV)
+    want_kept, want_n = O.evict(c.lens, c.table, 32, c.host, c.w, dst, 32, 16)
+    sda.sda_cache_evict(c.p, *c.args(), c.w_dev, dev(dst), kept, n, c.ws.ptr, c.ws.nbytes)
+    c.ws.check()
+    assert np.array_equal(kept.cpu().numpy(), want_kept) and np.array_equal(n.cpu().numpy(), want_n)
+    c.check_pool()
+    c.lens = lens
+    O.append(f64(k), f64(v), c.seq, c.lens, c.table, 32, c.host)
+    c.append(k, v, w=False)
+    c.ws.check()
+    c.check_pool()
