@@ -1083,7 +1083,7 @@ cudaError_t run_attn(const Cache& c, const Args& a, const CUtensorMap& mk, const
 
 template <int D>
 cudaError_t run(const Cache& c, const Args& a, const uint8_t* k_codes, const uint8_t* v_codes, const float* w_in,
-                float* w_out, cudaStream_t stream) {
+                float* w_out, bool wide_join, cudaStream_t stream) {
   if (encode_fn() == nullptr) return cudaErrorNotSupported;
   CUtensorMap mk, mv;
   if (!make_map(&mk, k_codes, c) || !make_map(&mv, v_codes, c)) return cudaErrorInvalidValue;
@@ -1092,13 +1092,10 @@ cudaError_t run(const Cache& c, const Args& a, const uint8_t* k_codes, const uin
                                : (one ? run_attn<D, 1, false>(c, a, mk, mv, stream) : run_attn<D, 2, false>(c, a, mk, mv, stream));
   if (e != cudaSuccess) return e;
   if (a.whole_row_tiles == 0) {
-    // A row's parts number about workers / units. A CTA per row costs many rows of few parts several waves, a
-    // warp per row costs few rows of many parts a chain of reads: the CTA from 16 parts on.
-    const int rows = c.B * c.H_kv * a.rows_pad;
-    const bool wide = a.workers >= 16 * c.B * c.H_kv * ((a.rows_pad + a.tile_rows - 1) / a.tile_rows);
-    e = wide ? launch_after(cache_join_kernel<D, true>, dim3(rows), dim3(kJoinThreads), 0, stream, c, a)
-             : launch_after(cache_join_kernel<D, false>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)),
-                            dim3(kJoinThreads), 0, stream, c, a);
+    const unsigned rows = static_cast<unsigned>(c.B * c.H_kv * a.rows_pad);  // below 2^31
+    e = wide_join ? launch_after(cache_join_kernel<D, true>, dim3(rows), dim3(kJoinThreads), 0, stream, c, a)
+                  : launch_after(cache_join_kernel<D, false>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)),
+                                 dim3(kJoinThreads), 0, stream, c, a);
     if (e != cudaSuccess) return e;
   }
   if (a.scores == nullptr) return cudaSuccess;
@@ -1138,6 +1135,9 @@ CacheLayout make_cache_layout(const Cache& c) {
   y.scores = off;   off = up(off + (c.weights ? static_cast<size_t>(heads) * tokens * y.rows_pad * 4 : 0));
   y.total = off;
   y.join_ctas = heads * y.rows_pad;
+  // A row's parts number about workers / units. A CTA per row costs many rows of few parts several waves, a
+  // warp per row costs few rows of many parts a chain of reads: the CTA from 16 parts on.
+  y.wide_join = y.workers >= 16 * heads * row_tiles;
   return y;
 }
 
@@ -1165,8 +1165,8 @@ cudaError_t launch_cache_attn(const Cache& c, const CacheLayout& y, void* ws, co
   a.whole_row_tiles = y.whole_row_tiles;
   a.rows_pad = y.rows_pad;
   a.wait_ns = serving_wait_limit();
-  if (c.d == 128) return run<128>(c, a, k_codes, v_codes, w_in, w_out, stream);
-  if (c.d == 64) return run<64>(c, a, k_codes, v_codes, w_in, w_out, stream);
+  if (c.d == 128) return run<128>(c, a, k_codes, v_codes, w_in, w_out, y.wide_join != 0, stream);
+  if (c.d == 64) return run<64>(c, a, k_codes, v_codes, w_in, w_out, y.wide_join != 0, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -53,6 +53,7 @@ struct CacheLayout {
   int rows_pad;                      // row slots per key head
   long long join_ctas;               // CTAs of the second kernel, at most
   long long line_places;             // the longest possible line of work
+  int wide_join;                     // 1: the second kernel takes a CTA per row, 0: a warp per row
 };
 CacheLayout make_cache_layout(const Cache& c);
 
