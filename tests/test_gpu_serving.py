@@ -894,3 +894,65 @@ def test_cache_scale_of_zero():
     c.append(k, v, w=False)
     c.ws.check()
     c.check_pool()
+
+
+def test_eviction_in_a_pool_of_more_than_4_gib():
+    """Sources and target behind the 32-bit byte offsets of the codes: codes, scales and weights of the target."""
+    n_blocks, H_kv, block, d = 300_000, 1, 128, 128
+    if torch.cuda.mem_get_info()[0] < 30e9:
+        pytest.skip("needs 30 GB of device memory")
+    rng = np.random.default_rng(34)
+    host = make_pool(rng, 4, H_kv, block, d)      # the last four blocks; 3 and 1 hold the tokens, 2 is the target
+    w = rng.random((4, H_kv, block)).astype(np.float32)
+    pool = {n: torch.zeros((n_blocks, *x.shape[1:]), dtype=torch.from_numpy(x).dtype, device=DEV) for n, x in host.items()}
+    w_dev = torch.zeros((n_blocks, H_kv, block), device=DEV)
+    for n, x in host.items():
+        pool[n][-4:] = dev(x)
+    w_dev[-4:] = dev(w)
+    low = {n: x[:4].clone() for n, x in pool.items()}
+    p = sda.cache_params(B=1, H=1, H_kv=H_kv, d=d, block=block, n_blocks=n_blocks, max_blocks=2, keep=100, recent=10)
+    ws = sda.Workspace(p)
+    table, dst, lens = np.array([[3, 1]], np.int32), np.array([[2]], np.int32), [200]
+    kept, n = torch.empty((1, 1, 100), dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    sda.sda_cache_evict(p, dev(np.array(lens, np.int32)), dev(table + n_blocks - 4), pool["k_codes"], pool["v_codes"],
+                        pool["k_scale"], pool["v_scale"], w_dev, dev(dst + n_blocks - 4), kept, n, ws.ptr, ws.nbytes)
+    ws.check()
+    want_kept, want_n = O.evict(lens, table, block, host, w, dst, 100, 10)
+    assert np.array_equal(kept.cpu().numpy(), want_kept) and np.array_equal(n.cpu().numpy(), want_n)
+    for m, x in pool.items():
+        assert np.array_equal(x[-4:].cpu().numpy(), host[m]), m
+        assert torch.equal(x[:4], low[m]), m      # where a 32-bit offset would have landed
+    assert np.array_equal(w_dev[-4:].cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("lens,weights", [([500] * 100, False), ([20000, 40], False), ([20000, 40, 7000], True)])
+def test_cache_wait_that_runs_out(lens, weights):
+    """With a limit of 0 some wait of many calls finds its load not landed: it is reported, every load of the CTA is
+    waited for, and the next call on the same workspace is right."""
+    rng = np.random.default_rng(35)
+    c = Cache(rng, lens, 32, 8, 2, 128, [1] * len(lens), weights=weights)
+    q = bf16((len(lens), 8, 128), rng).to(DEV)
+    w_out = torch.zeros(c.w.shape, device=DEV) if weights else None
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)      # the cache leaves L2: its loads take their time
+    want = c.attend(q, None, w_out)
+    c.ws.check()
+    want_w = w_out.clone() if weights else None
+    before = sda.sda_set_attention_wait_limit_ns(0)
+    ran_out = 0
+    try:
+        for _ in range(50):
+            flush.zero_()
+            c.attend(q, None, w_out)
+            try:
+                c.ws.check()
+            except sda.SdaError as e:
+                assert e.code == -7
+                ran_out += 1
+                if ran_out == 3:
+                    break
+    finally:
+        sda.sda_set_attention_wait_limit_ns(before)
+    assert ran_out, "no wait ran out in 50 calls"
+    assert torch.equal(c.attend(q, None, w_out), want)
+    c.ws.check()
+    assert not weights or torch.equal(w_out, want_w)
