@@ -7,9 +7,10 @@
 //
 // Both are bound by memory: append reads the new rows (bf16) and writes their
 // codes, eviction reads the weights of every token and moves the kept rows.
-// Measured: 13,600 tokens of 6 prompts, 8 heads: 20 us (2.8 TB/s; 8.5 us at the
-// measured copy rate); one token for 64 sequences: 7.6 us, a launch and a chain
-// of four reads; 32 sequences of 6,000 to 16,384 tokens to 4,096, 8 heads: 134 us
+// Measured: 9,076 tokens, 9,001 of them to one of 6 sequences, 8 heads: 20 us
+// (2.8 TB/s; 8.5 us at the measured copy rate); 6 whole prompts of 1,500 tokens:
+// 13.3 us, 4 tokens for each of 64 sequences 7.8 us, one for each 6.7 us, a
+// launch and a chain of four reads; 32 sequences of 6,000 to 16,384 tokens to 4,096, 8 heads: 134 us
 // (85 us at the copy rate), 31 us of it the selection, whose instructions bound it,
 // and 105 us the move (5.2 TB/s).
 
@@ -407,9 +408,11 @@ cudaError_t launch_cache_append(const Cache& c, const uint16_t* k, const uint16_
                                 float* k_scale, float* v_scale, float* w, unsigned* status, cudaStream_t stream) {
   const int most = min(c.max_new, c.rows);
   const int touched = (most + c.block - 2) / c.block + 1;  // blocks that `most` tokens can lie in
-  // Single tokens: a CTA per unit, for latency. Prompts: four units a CTA, since most CTAs of a batch of unequal
-  // prompts find nothing to do (6 prompts of 300 to 9,001 tokens: 26 us with one unit, 20 us with four).
-  const int units = touched > 1 ? 4 : 1;
+  // Single tokens: a CTA per unit, for latency. More tokens can touch a block more than they do, so that half of the
+  // CTAs or more find nothing to do: two units a CTA (8 heads; us with one, two and four units: 64 sequences of 4 new
+  // tokens 8.6, 7.8, 12.2; of 17: 10.2, 10.0, 12.9; of 200: 26.1, 23.9, 24.5; 6 of 1,500: 14.3, 13.3, 13.4; one of
+  // 9,001 beside five of 5 to 25: 24.4, 20.3, 19.9; and 64 of one token: 6.7, 6.8 with two).
+  const int units = touched > 1 ? 2 : 1;
   const dim3 grid(static_cast<unsigned>(touched) * ((2 * c.H_kv + units - 1) / units), c.B);
   const int threads = c.block * c.d / 8 / kPasses;
   return launch_after(c.d == 128 ? cache_append_kernel<128> : cache_append_kernel<64>, grid, dim3(threads), 0, stream, c,
