@@ -133,23 +133,28 @@ __device__ __forceinline__ int tiles_over(const Prompt& p, const Span& s, int lr
   return T - min(first, T - 1);
 }
 
-// The CTA's row tile. Tiles go out heaviest first (most key steps), so that
+// The CTA's row tiles. Tiles go out heaviest first (most key steps), so that
 // the last ones to start are short: tile i of the order has the step count x
 // with over(x) <= i < over(x - 1), over(x) the number of tiles of more than x
-// steps, found by bisection; among equals, sequences in order.
-__device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int lr, int i, Item* out,
+// steps, found by bisection; among equals, sequences in order. A CTA asks for
+// ascending i, so the count x and the place among the sequences go on from the
+// tile before: the offsets are read a few times for each count that occurs,
+// not for each tile (4,096 prompts of 100 tokens, 32 heads over 8, d = 128:
+// 2.9 ms, 33.7 with a search of its own for each tile).
+struct Search {
+  int x, lo, hi;      // the count of tiles lo .. hi - 1 of the order; hi = 0 before the first
+  int base, before;   // of them, `before` belong to the sequences before `base`
+};
+__device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* seq_k, int lr, int i, Search& at, Item* out,
                           bool& bad) {
   const int lane = threadIdx.x & 31;
-  Span mine{0, 0, 0, 0};
+  Span mine{0, 0, 0, 0};  // of the first 32 sequences
   if (lane < p.n_seq) mine = span_of(p, seq_q, seq_k, lane, bad);
   auto over = [&](int x) {
     int n = lane < p.n_seq ? tiles_over(p, mine, lr, x) : 0;
     for (int s = 32 + lane; s < p.n_seq; s += 32) n += tiles_over(p, span_of(p, seq_q, seq_k, s, bad), lr, x);
     return __reduce_add_sync(0xffffffffu, n);
   };
-  int top = lane < p.n_seq ? mine.nk : 0;
-  for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
-  top = __reduce_max_sync(0xffffffffu, top);
   // one lane says that there is none, in order before the lane that finds it: the warp need not be converged
   if (lane == 0) out->valid = 0;
   __syncwarp();
@@ -158,26 +163,35 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
     if (lane == 0 && i < T) *out = Item{1, mine.q0, mine.nq, mine.k0, mine.nk, T - 1 - i};
     return;
   }
-  if (i >= over(-1)) return;
-  int lo = 0, hi = (top + kTile - 1) / kTile;  // over(hi) = 0 <= i
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (over(mid) <= i) hi = mid;
-    else lo = mid + 1;
+  if (i >= at.hi) {
+    int least = 0, most = at.x;  // the next count is one of these
+    if (at.hi == 0) {            // the first tile
+      int top = lane < p.n_seq ? mine.nk : 0;
+      for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
+      most = (__reduce_max_sync(0xffffffffu, top) + kTile - 1) / kTile;  // over(most) = 0 <= i
+    }
+    at.hi = over(-1);
+    if (i >= at.hi) return;      // behind the last
+    while (least < most) {
+      const int mid = (least + most) / 2;
+      if (over(mid) <= i) most = mid;
+      else least = mid + 1;
+    }
+    at = Search{least, over(least), over(least - 1), 0, 0};
   }
-  int rest = i - over(lo);  // number among the tiles of exactly lo steps
-  for (int base = 0; base < p.n_seq; base += 32) {
-    const int s = base + lane;
-    Span sp = base == 0 ? mine : Span{0, 0, 0, 0};
-    if (base > 0 && s < p.n_seq) sp = span_of(p, seq_q, seq_k, s, bad);
-    const int above = s < p.n_seq ? tiles_over(p, sp, lr, lo) : 0;
-    const int n = s < p.n_seq ? tiles_over(p, sp, lr, lo - 1) - above : 0;
+  while (at.base < p.n_seq) {
+    const int s = at.base + lane;
+    Span sp = at.base == 0 ? mine : Span{0, 0, 0, 0};
+    if (at.base > 0 && s < p.n_seq) sp = span_of(p, seq_q, seq_k, s, bad);
+    const int above = s < p.n_seq ? tiles_over(p, sp, lr, at.x) : 0;
+    const int n = s < p.n_seq ? tiles_over(p, sp, lr, at.x - 1) - above : 0;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += u;
     }
+    const int rest = i - at.lo - at.before;  // number among the tiles of this count from `base` on
     if (rest >= sum - n && rest < sum) {
       out->q0 = sp.q0;
       out->nq = sp.nq;
@@ -188,7 +202,8 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
     }
     const int all = __shfl_sync(0xffffffffu, sum, 31);
     if (rest < all) break;
-    rest -= all;
+    at.before += all;
+    at.base += 32;
   }
 }
 
@@ -432,13 +447,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       tc::wait_warp(&bars[B_DRAIN], 0, &never);
     } else if (warp == 2) {
       // ------------------------------------------------------------ items, one ahead of their use
+      Search at{0, 0, 0, 0, 0};
       for (int r = 0;; ++r) {
         if (r >= 2) ok = tc::wait_warp(&bars[B_TAKEN + (r & 1)], ((r >> 1) - 1) & 1, abort_flag, wait_ns);
         if (!ok) break;
         bool bad = false;
         const long long tile = number(r) / groups;
         find_item(p, seq_q, seq_k, pair_heads ? 7 : 8, static_cast<int>(min(tile, static_cast<long long>(INT_MAX))),
-                  &items[r & 1], bad);
+                  at, &items[r & 1], bad);
         if (r == 0 && blockIdx.x == 0 && __any_sync(0xffffffffu, bad) && lane == 0) report_status(status, kStatusBadIndex);
         __syncwarp();
         const int valid = *reinterpret_cast<volatile int*>(&items[r & 1].valid);

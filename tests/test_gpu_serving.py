@@ -956,3 +956,37 @@ def test_cache_wait_that_runs_out(lens, weights):
     assert torch.equal(c.attend(q, None, w_out), want)
     c.ws.check()
     assert not weights or torch.equal(w_out, want_w)
+
+
+@pytest.mark.parametrize("n_seq,H,H_kv,causal", [(1500, 2, 1, True), (1500, 1, 1, False), (20000, 2, 2, True)])
+def test_prompt_thousands_of_sequences(n_seq, H, H_kv, causal):
+    """Mostly a few tokens each, some empty, some of several tiles, so that a CTA goes through many step counts and
+    groups of sequences."""
+    rng = np.random.default_rng(36)
+    n = rng.integers(0, 7, n_seq)
+    n[rng.integers(0, n_seq, 8)] = [600, 300, 290, 257, 256, 129, 128, 127]
+    nk = n if causal else rng.integers(0, 7, n_seq)
+    sq, sk = offsets(n), offsets(nk)
+    q, k, v = (bf16((int(a[-1]), h, 64), rng).to(DEV) for a, h in ((sq, H), (sk, H_kv), (sk, H_kv)))
+    o, lse = run_prompt(q, k, v, sq, sk, causal)
+    check_prompt(q, k, v, sq, sk, causal, o, lse)
+
+
+def test_prompt_time_is_linear_in_the_number_of_sequences():
+    """16 times as many prompts of 100 tokens take about 16 times as long, the search for a CTA's tiles with them."""
+    def time(n):
+        q, k, v = (torch.randn(n * 100, h, 64, device=DEV).to(torch.bfloat16) for h in (32, 8, 8))
+        p = sda.prompt_params(n_seq=n, rows_q=n * 100, rows_k=n * 100, H=32, H_kv=8, d=64)
+        ws, seq, o = sda.Workspace(p), torch.arange(n + 1, dtype=torch.int32, device=DEV) * 100, torch.empty_like(q)
+        best = float("inf")
+        for _ in range(5):
+            a, b = torch.cuda.Event(True), torch.cuda.Event(True)
+            a.record()
+            sda.sda_prompt_attn_fwd(p, q, k, v, seq, seq, o, None, ws.ptr, ws.nbytes)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        ws.check()
+        return best
+    few, many = time(256), time(4096)
+    assert many < 3 * 16 * few, (few, many)       # 130 times when each tile's search read all offsets anew
