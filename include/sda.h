@@ -351,7 +351,7 @@ size_t sda_prompt_workspace_size(const sda_prompt_params* p);
  * [rows_q, H] fp32 or NULL. k and v rows of a sequence must be finite (a
  * hidden key's infinity may reach rows that do not see it); rows outside the
  * sequences may hold anything. Bad offsets: the sequences' outputs are
- * undefined. */
+ * undefined (nothing is computed where sequences overlap by many tiles). */
 int32_t sda_prompt_attn_fwd(const sda_prompt_params* p, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                             const int32_t* seq_q, const int32_t* seq_k, uint16_t* o, float* lse, void* ws,
                             size_t ws_bytes, void* stream);

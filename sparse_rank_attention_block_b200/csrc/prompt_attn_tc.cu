@@ -91,6 +91,7 @@ enum {  // w: tile (two each); an item's barriers two each, by its number
   B_QFULL = 0, B_QFREE = 2, B_SFULL = 4, B_PFULL = 6, B_ODONE = 8, B_OFREE = 10, B_ITEM = 12, B_TAKEN = 14, B_DRAIN = 16,
   B_FULL = 17  // ring full, then ring empty
 };
+constexpr int kManyTiles = 1 << 24;  // a lane's count of tiles, at most: more than ascending offsets can have
 constexpr int kConsumers = 10;  // of an item: loader, MMA warp, 8 softmax warps
 
 // What the CTA works on, found by one warp.
@@ -152,7 +153,8 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   if (lane < p.n_seq) mine = span_of(p, seq_q, seq_k, lane, bad);
   auto over = [&](int x) {
     int n = lane < p.n_seq ? tiles_over(p, mine, lr, x) : 0;
-    for (int s = 32 + lane; s < p.n_seq; s += 32) n += tiles_over(p, span_of(p, seq_q, seq_k, s, bad), lr, x);
+    for (int s = 32 + lane; s < p.n_seq; s += 32)
+      n = min(n + tiles_over(p, span_of(p, seq_q, seq_k, s, bad), lr, x), kManyTiles);
     return __reduce_add_sync(0xffffffffu, n);
   };
   // one lane says that there is none, in order before the lane that finds it: the warp need not be converged
@@ -166,9 +168,16 @@ __device__ void find_item(const Prompt& p, const int32_t* seq_q, const int32_t* 
   if (i >= at.hi) {
     int least = 0, most = at.x;  // the next count is one of these
     if (at.hi == 0) {            // the first tile
-      int top = lane < p.n_seq ? mine.nk : 0;
-      for (int s = 32 + lane; s < p.n_seq; s += 32) top = max(top, span_of(p, seq_q, seq_k, s, bad).nk);
-      most = (__reduce_max_sync(0xffffffffu, top) + kTile - 1) / kTile;  // over(most) = 0 <= i
+      int top = lane < p.n_seq ? (mine.nk + kTile - 1) / kTile : 0, sum = top;
+      for (int s = 32 + lane; s < p.n_seq; s += 32) {
+        const int n = (span_of(p, seq_q, seq_k, s, bad).nk + kTile - 1) / kTile;
+        top = max(top, n);
+        sum = min(sum + n, kManyTiles);
+      }
+      most = __reduce_max_sync(0xffffffffu, top);  // over(most) = 0 <= i
+      // Ascending offsets leave no more tiles than this. Others are reported by then, and whatever they hold, they do
+      // not make the work a multiple of what the tensors have.
+      if (__reduce_add_sync(0xffffffffu, sum) > p.rows_k / kTile + p.n_seq || over(-1) > (p.rows_q >> lr) + p.n_seq) return;
     }
     at.hi = over(-1);
     if (i >= at.hi) return;      // behind the last

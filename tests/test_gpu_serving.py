@@ -990,3 +990,26 @@ def test_prompt_time_is_linear_in_the_number_of_sequences():
         return best
     few, many = time(256), time(4096)
     assert many < 3 * 16 * few, (few, many)       # 130 times when each tile's search read all offsets anew
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_prompt_overlapping_sequences_are_no_work(which):
+    """Offsets that go up and down would make every second sequence all the rows: the work stays that of the tensors,
+    here none, and the offsets are reported."""
+    rng = np.random.default_rng(37)
+    T, n_seq = 5000, 40
+    q, k, v = (bf16((T, h, 64), rng).to(DEV) for h in (2, 1, 1))
+    p = sda.prompt_params(n_seq=n_seq, rows_q=T, rows_k=T, H=2, H_kv=1, d=64)
+    ws = sda.Workspace(p)
+    seq = [dev(offsets([T // n_seq] * n_seq))] * 2
+    seq[which] = dev(np.array([0, T] * 20 + [0], np.int32))
+    o, lse = torch.full_like(q, 7.0), torch.full((T, 2), 7.0, device=DEV)
+    sda.sda_prompt_attn_fwd(p, q, k, v, *seq, o, lse, ws.ptr, ws.nbytes)
+    with pytest.raises(sda.SdaError) as e:
+        ws.check()
+    assert e.value.code == -3
+    assert torch.all(o == 7) and torch.all(lse == 7)
+    seq[which] = seq[1 - which]
+    sda.sda_prompt_attn_fwd(p, q, k, v, *seq, o, lse, ws.ptr, ws.nbytes)
+    ws.check()
+    check_prompt(q, k, v, seq[0].cpu().numpy(), seq[1].cpu().numpy(), True, o, lse)
