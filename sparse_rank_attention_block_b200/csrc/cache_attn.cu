@@ -1,5 +1,7 @@
-// Attention over the 8-bit key/value cache, for the few newest tokens of each
-// sequence.
+// Attention over the 8-bit key/value cache, for the newest tokens of each
+// sequence: made for a few of them. Any number is right, but every 16 query rows
+// of a key head read and convert the cache anew (a chunk of 1,560 tokens over
+// 32,768, 32 heads over 8: 4.4 ms, 186 TFLOP/s).
 //
 //   s_rj = scale * ks_j (q_r . kc_j),  o_r = sum_j p_rj vs_j vc_j,
 //   p_rj = exp(s_rj) / sum_j' exp(s_rj')
@@ -21,8 +23,8 @@
 // maximum, sum and output (no barrier between warps), merged where the unit or
 // the stretch ends. Where a stretch holds all tiles of a unit the CTA writes the
 // output; where it holds a part, a partial sum, which a second kernel joins in
-// the order of the line. That kernel also turns the scores of the first into
-// the tokens' weights (a probability needs the sum over all tokens). Where no
+// the order of the line. A third turns the scores of the first into the tokens'
+// weights (a probability needs the sum over all tokens). Where no
 // sequence can have more than kWholeTiles tiles, a CTA takes one whole unit.
 //
 // Scales differ from block to block. K's multiplies the scores. V's goes into
@@ -37,8 +39,9 @@
 // precision is 2^-11 of every term down to 2^-77 of the maximum, and what is
 // below 2^-88 counts as zero. The passes cost such a tile its conversions and
 // MMAs again (131,072 tokens, 4 rows to a key head, every tile of this kind: 69
-// against 62.5 us); elsewhere they are a test of the least operand (16 sequences
-// of up to 4 new tokens 33.9 against 33.0 us, the other cases within the noise).
+// against 62.5 us); elsewhere they are a test of the least operand and code to
+// fetch (one sequence of 300 tokens 6.2 against 5.5 us, 16 sequences of 1 to 4
+// new tokens 33.6 against 32.9 us, long ones within the noise).
 // The first pass stands apart from the rare ones: in one loop with them it costs
 // the loads their head start (131,072 tokens 54.4 against 52.1 us).
 //
@@ -53,7 +56,7 @@
 // (5.2 TB/s; 41 us at the measured copy rate), 64 sequences of 500 to 16,000
 // tokens with weights 137 us (97 us), of which the first kernel takes 117, the
 // join 6, the weights 16. Two CTAs of three stages an SM against three of two:
-// 52.6 and 54.3 us (long), 33.0 and 37.9 us (16 sequences, 4 new tokens).
+// 52.6 and 54.3 us (long), 33.0 and 37.9 us (16 sequences, 1 to 4 new tokens).
 //
 // Tokens that a row must not see get a score of -inf; V codes of tokens behind
 // the sequence (free slots, holding anything) are cleared before use.
@@ -81,7 +84,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kSms = 148;
 constexpr int kLeast = 8;      // places of a stretch, at least
 // What a unit costs before its first tile (block numbers, scales, Q, the merge at its end: each a chain of
-// reads), in tiles: places without a tile at its start. 16 sequences of 33 to 6,000 tokens, 4 new tokens each:
+// reads), in tiles: places without a tile at its start. 16 sequences of 33 to 6,000 tokens, 1 to 4 new ones each:
 // 40.9, 37.9, 36.6 and 41.0 us with 4, 8, 16 and 32; 64 sequences of 500 to 16,000: 139.9, 137.7, 140.0, 141.9 us.
 constexpr int kLead = 8;
 constexpr int kWholeTiles = 16;
@@ -180,12 +183,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-// The smaller of each pair of fp16 values, a NaN only where both are.
-__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 __device__ __forceinline__ constexpr float exp2_of(int e) {  // -126 <= e <= 127
   return __builtin_bit_cast(float, static_cast<uint32_t>(e + 127) << 23);
@@ -562,7 +559,7 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
       float p[NR][2][4];              // 2^(s + lv - mv + kUp)
       uint32_t pf[NR][2][2];          // P^T fragments of the two 16-token steps
-      bool small = false;             // some p below kLeastP (or a token that is not seen)
+      bool small = false;             // some p below kLeastP, but not zero
       bool far = false;               // some p too far above its 2^(s - m)
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr) {
@@ -586,8 +583,10 @@ cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           pf[nr][hf][0] = pack_f16(p[nr][hf][0], p[nr][hf][1]);
           pf[nr][hf][1] = pack_f16(p[nr][hf][2], p[nr][hf][3]);
         }
-        const uint32_t least = min_f16x2(min_f16x2(pf[nr][0][0], pf[nr][0][1]), min_f16x2(pf[nr][1][0], pf[nr][1][1]));
-        small = small || far || (least & 0x7c00u) == 0u || (least & 0x7c000000u) == 0u;
+        uint32_t least = ~0u;         // of the bits less one: what is zero (a token not seen) comes last
+#pragma unroll
+        for (int e = 0; e < 8; ++e) least = min(least, __float_as_uint(p[nr][e / 4][e % 4]) - 1u);
+        small = small || far || least < __float_as_uint(kLeastP) - 1u;
       }
       // Terms that fp16 does not hold in full are left to further passes, each 2^kBand up (exactly, the output so far
       // with them): a dominant token whose V is small leaves the output to them.
