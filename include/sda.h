@@ -403,7 +403,8 @@ int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uin
  * max_new) is its token lens[b] - n_b + i and sees tokens 0 .. that one (append
  * its key first): o as in sda_prompt_attn_fwd, with the cache's values; a row
  * at a negative position sees nothing and gets zeros. Products of q (bf16,
- * brought to fp16 by an exact power of two per row) with the codes are exact.
+ * brought to fp16 by a power of two per row, which is exact but for elements
+ * 2^-31 of the row's largest and below) with the codes are exact.
  * P times V's scale is rounded to fp16's 11 digits, term by term down to 2^-77
  * of the row's largest such term; below 2^-88 of it a term counts as zero.
  * w_out (or NULL; needs weights = 1): w_out[slot] = w_in[slot] + the sum of the token's p over the
@@ -411,8 +412,11 @@ int32_t sda_cache_append(const sda_cache_params* p, const uint16_t* k, const uin
  * sequences; other slots of w_out stay as they are. w_in NULL counts as zeros;
  * w_in may be w_out. Sequences may share blocks when w_out is NULL; with it a
  * block belongs to one sequence. Rows over max_new, tokens in blocks outside the pool and
- * tokens past max_blocks * block are left out and reported. NaN or infinity in a
- * cached token reaches the rows of its sequence. */
+ * tokens past max_blocks * block are left out and reported. NaN in a
+ * cached token reaches the rows of its sequence.
+ * The call is made for a few new tokens: every 16 rows of a key head (new
+ * tokens times H / H_kv) read that head's cache anew, and with weights = 1 the
+ * workspace holds a score for each of B * H_kv * max_blocks * block * rows. */
 int32_t sda_cache_attn_fwd(const sda_cache_params* p, const uint16_t* q, const int32_t* seq, const int32_t* lens,
                            const int32_t* block_table, const uint8_t* k_codes, const uint8_t* v_codes,
                            const float* k_scale, const float* v_scale, const float* w_in, float* w_out,
@@ -421,7 +425,9 @@ int32_t sda_cache_attn_fwd(const sda_cache_params* p, const uint16_t* q, const i
 /* Eviction by collected weight. For every sequence b and key head: of its
  * lens[b] tokens n = min(lens[b], keep) stay: the newest min(recent, n) and,
  * of the older ones, those with the largest w (ties to the lower position; NaN
- * counts as the largest). They keep their order and become tokens 0 .. n - 1 of
+ * counts as the largest; append sets w to zero and prompt attention collects
+ * none, so give a prompt's last rows to sda_cache_attn_fwd before its first
+ * eviction). They keep their order and become tokens 0 .. n - 1 of
  * the blocks dst_table[b, :] ([B, ceil(keep / block)], other blocks than those
  * of block_table; n tokens' blocks are read, the rest may be -1). A target
  * block's scale is the largest of its tokens' source scales, codes are written
@@ -442,10 +448,12 @@ int32_t sda_cache_evict(const sda_cache_params* p, const int32_t* lens, const in
  * returns the previous limit. The default is 2e9 (2 s, far beyond any
  * legitimate wait). 0 makes a wait give up unless its phase is already
  * complete at the first, non-blocking test, so a launch then reliably takes
- * the failure path: the CTA records SDA_ERR_TIMEOUT in the workspace status
+ * the failure path (sda_cache_attn_fwd: where a load has not landed): the CTA
+ * records SDA_ERR_TIMEOUT in the workspace status
  * word (sda_read_status), waits -- with the 2 s limit -- for its own TMA
  * loads and MMAs in flight, frees its tensor memory and exits; its outputs are
- * undefined, and later launches skip their work until the status is read.
+ * undefined, and later launches skip their work until the status is read (the
+ * cache's calls do not: they run as ever).
  * Meant for tests of that path; not for production use. */
 uint64_t sda_set_attention_wait_limit_ns(uint64_t limit_ns);
 

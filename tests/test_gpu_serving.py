@@ -1013,3 +1013,59 @@ def test_prompt_overlapping_sequences_are_no_work(which):
     sda.sda_prompt_attn_fwd(p, q, k, v, *seq, o, lse, ws.ptr, ws.nbytes)
     ws.check()
     check_prompt(q, k, v, seq[0].cpu().numpy(), seq[1].cpu().numpy(), True, o, lse)
+
+
+def test_cache_weights_of_a_prompts_last_rows_decide_its_first_eviction():
+    """Whole prompts appended (weights zero), their last rows through cache attention, an eviction by those weights,
+    then a token on the blocks that stayed: the order of calls that the header asks for."""
+    rng = np.random.default_rng(38)
+    H, H_kv, d, block, n, last, keep, recent = 8, 2, 64, 16, [150, 40, 300], 16, 64, 8
+    c = Cache(rng, n, block, H, H_kv, d, n, extra=20, keep=keep, recent=recent)
+    q, k, v = (bf16((sum(n), h, d), rng).to(DEV) for h in (H, H_kv, H_kv))
+    O.append(f64(k), f64(v), c.seq, c.lens, c.table, block, c.host, c.w)
+    c.append(k, v)
+    c.ws.check()
+    c.check_pool()
+    assert np.array_equal(c.w_dev.cpu().numpy(), c.w)
+    free = [b for b in range(c.n_blocks) if b not in c.table]
+    wide = np.full((3, 5), -1, np.int32)                          # a block more than `keep` needs
+    for b, t in enumerate(n):
+        need = -(-(min(t, keep) + 1) // block)
+        wide[b, :need], free = free[:need], free[need:]
+    dst = np.ascontiguousarray(wide[:, :4])
+    q_last = torch.cat([q[a - last:a] for a in c.seq[1:]])
+
+    def call(table, rows):
+        c.p = sda.cache_params(B=3, H=H, H_kv=H_kv, d=d, block=block, n_blocks=c.n_blocks, max_blocks=table.shape[1],
+                               rows=3 * rows, max_new=rows, weights=True, keep=keep, recent=recent)
+        c.ws, c.table, c.seq = sda.Workspace(c.p), table, offsets([rows] * 3)
+
+    call(c.table, last)
+    o = c.attend(q_last, c.w_dev, c.w_dev)
+    c.ws.check()
+    want, spread, wt = O.cache_attention(f64(q_last), c.seq, c.lens, c.table, block, c.host)
+    size = max(score_size(f64(q_last), O.cache_values(c.host, "k", c.table[b], t, block, h))
+               for b, t in enumerate(n) for h in range(H_kv))
+    assert np.all(np.abs(f64(o) - want) <= attention_tolerance(want, spread, size, d, U_F16))
+    got_w = c.w_dev.cpu().numpy()
+    p_error = 2 * (2 * (d + 8) * U_F32 * size + 2.0 ** -20)
+    for b, t in enumerate(n):
+        i = np.arange(t)
+        got = got_w[c.table[b, i // block], :, i % block].T
+        assert np.all(np.abs(got - wt[b]) <= wt[b] * (p_error + (last * (H // H_kv) + 2) * U_F32))
+    kept, m = torch.empty((3, H_kv, keep), dtype=torch.int32, device=DEV), torch.empty(3, dtype=torch.int32, device=DEV)
+    sda.sda_cache_evict(c.p, *c.args(), c.w_dev, dev(dst), kept, m, c.ws.ptr, c.ws.nbytes)
+    c.ws.check()
+    c.w = got_w
+    want_kept, want_m = O.evict(c.lens, c.table, block, c.host, c.w, dst, keep, recent)
+    assert np.array_equal(kept.cpu().numpy(), want_kept) and np.array_equal(m.cpu().numpy(), want_m)
+    assert want_kept[0, 0, :keep - recent].max() >= keep - recent  # not merely the oldest: the weights decided
+    c.check_pool()
+    assert np.array_equal(c.w_dev.cpu().numpy(), c.w)
+    call(wide, 1)
+    c.lens = [int(x) + 1 for x in want_m]
+    q1, k1, v1 = (bf16((3, h, d), rng).to(DEV) for h in (H, H_kv, H_kv))
+    O.append(f64(k1), f64(v1), c.seq, c.lens, c.table, block, c.host, c.w)
+    c.append(k1, v1)
+    c.check_pool()
+    check_cache_attention(c, q1)
