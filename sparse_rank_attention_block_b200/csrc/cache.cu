@@ -8,11 +8,12 @@
 // Both are bound by memory: append reads the new rows (bf16) and writes their
 // codes, eviction reads the weights of every token and moves the kept rows.
 // Measured: 9,076 tokens, 9,001 of them to one of 6 sequences, 8 heads: 20 us
-// (2.8 TB/s; 8.5 us at the measured copy rate); 6 whole prompts of 1,500 tokens:
-// 13.3 us, 4 tokens for each of 64 sequences 7.8 us, one for each 6.7 us, a
-// launch and a chain of four reads; 32 sequences of 6,000 to 16,384 tokens to 4,096, 8 heads: 134 us
-// (85 us at the copy rate), 31 us of it the selection, whose instructions bound it,
-// and 105 us the move (5.2 TB/s).
+// (2.8 TB/s; 8.5 us at the measured copy rate); from inputs in L2: 6 whole
+// prompts of 1,500 tokens 13.4 us, 4 tokens for each of 64 sequences 7.7 us, one
+// for each 6.7 us, a launch and a chain of four reads. Eviction of 32 sequences
+// of 6,000 to 16,384 tokens to 4,096, 8 heads: 134 us (85 us at the copy rate),
+// 31 us of it the selection, whose instructions bound it, and 106 us the move
+// (5.2 TB/s).
 
 #include "common.cuh"
 #include "e4m3.cuh"

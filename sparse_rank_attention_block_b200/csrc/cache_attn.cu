@@ -54,7 +54,7 @@
 //
 // Measured (32 heads over 8, d = 128): one sequence of 131,072 tokens 52 us
 // (5.2 TB/s; 41 us at the measured copy rate), 64 sequences of 500 to 16,000
-// tokens with weights 137 us (97 us), of which the first kernel takes 117, the
+// tokens with weights 137 us (97 us), of which the first kernel takes 115, the
 // join 6, the weights 16. Two CTAs of three stages an SM against three of two:
 // 52.6 and 54.3 us (long), 33.0 and 37.9 us (16 sequences, 1 to 4 new tokens).
 //

@@ -34,7 +34,7 @@
 // opposite phase; an issuer for each tile let them fall into step, both in the
 // exponentials and then both in the MMAs (4,230 cycles for a pair of steps).
 // Handing P over in two halves cost more in waits than it overlapped (+4 %), and
-// taking a share of the exponentials on the FMA pipe lost 4 to 8 %.
+// taking a share of the exponentials on the FMA pipe lost 4 to 8 % (d = 128).
 //
 // Measured: one sequence of 16,384 tokens, 16 heads over 4, causal: 1.04 ms,
 // 1,055 TFLOP/s (0.65 of the measured burst peak; clocks fall to 1.53 GHz
